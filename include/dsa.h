@@ -137,6 +137,20 @@ enum {
   DSA_SELECT_IN_INDEXER = 1
 };
 
+/* Element types of dsa_rope. */
+enum {
+  DSA_ROPE_BF16 = 0,
+  DSA_ROPE_F16 = 1,
+  DSA_ROPE_F32 = 2
+};
+/* Flags and limit of dsa_rope. */
+enum {
+  DSA_ROPE_HALF = 1,      /* pair j = dims j, j + rot_dim/2 (else 2j, 2j + 1)        */
+  DSA_ROPE_TRANSPOSE = 2, /* the transposed map: the gradient of the rotation        */
+  DSA_ROPE_POS64 = 4,     /* positions are int64 (else int32)                        */
+  DSA_ROPE_MAX_DIM = 1024 /* the largest rot_dim                                     */
+};
+
 /* Batch geometry (host struct; the three arrays are device memory).
  *   batch          B >= 1 sequences
  *   num_q_tokens   T = q_seq_start[B] >= 1 (host copy of the last entry)
@@ -329,6 +343,31 @@ dsa_status_t dsa_index_topk_attn_ex(const dsa_seqs_t *seqs, const void *qI,
                                     int32_t *idx_out, void *ws, size_t ws_bytes,
                                     unsigned flags, dsa_event_t q_ready,
                                     dsa_stream_t stream);
+
+/* Rotary positions, the input preparation of the queries and keys ([P2]
+ * section 4(2) prepares them ahead of the indexer and the attention: the rope
+ * dims 512..575 of q and of the latent rows, and those of the index vectors).
+ * Dims offset .. offset + rot_dim - 1 of every (token, head) row are rotated
+ * pair by pair: pair j, (a, b), becomes
+ *   amplitude * (a cos - b sin, a sin + b cos),  angle = 2 pi positions[t] turns[j] / 2^64.
+ * The other dims are copied; out may be x itself (same pointer and strides),
+ * which leaves them alone.  With DSA_ROPE_TRANSPOSE sin is negated.
+ *   x, out     [T, H, D] of `dtype`, last dim contiguous, other strides in
+ *              elements (out's rows disjoint; x and out the same view, or no
+ *              element in common); element-aligned (16-byte vectors are used
+ *              where pointers, strides, offset and dims are multiples of 16 B)
+ *   positions  int32 or int64 (DSA_ROPE_POS64) [T], any value, negative too
+ *   turns      uint64 [rot_dim / 2], the frequencies in units of 2^-64 turn per
+ *              position (a wrapping product: exact at any position)
+ *   rot_dim    even, 2 .. DSA_ROPE_MAX_DIM, offset + rot_dim <= D
+ * fp32 arithmetic, one rounding to dtype.  No workspace; T = 0 launches
+ * nothing.  Errors: DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED / DSA_ERR_CUDA. */
+dsa_status_t dsa_rope(const void *x, void *out, int dtype, int T, int H, int D,
+                      int64_t x_stride_t, int64_t x_stride_h,
+                      int64_t out_stride_t, int64_t out_stride_h,
+                      const void *positions, const uint64_t *turns, int rot_dim,
+                      int offset, float amplitude, unsigned flags,
+                      dsa_stream_t stream);
 
 /* Synchronises `stream`, reads and clears the workspace's sticky device error
  * flag.  Returns DSA_OK, DSA_ERR_BAD_INDEX, DSA_ERR_TIMEOUT or DSA_ERR_CUDA

@@ -19,6 +19,7 @@ from dataclasses import dataclass
 import torch
 
 from . import build as _build
+from .rope import RopeTable
 
 # ---------------------------------------------------------------------------
 # Library loading
@@ -38,6 +39,8 @@ DSA_NOALLOC_SCRATCH_BYTES = 32 << 20
 DSA_OP_QUANTIZE_INDEX_QUERY, DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_INDEX_TOPK_ATTN, \
     DSA_OP_INDEX_TOPK_ATTN_FUSED = range(6)
 DSA_SELECT_IN_INDEXER = 1
+DSA_ROPE_BF16, DSA_ROPE_F16, DSA_ROPE_F32 = range(3)
+DSA_ROPE_HALF, DSA_ROPE_TRANSPOSE, DSA_ROPE_POS64, DSA_ROPE_MAX_DIM = 1, 2, 4, 1024
 
 # Names the C header declares (checked against include/dsa.h by the tests).
 EXPORTS = ("dsa_workspace_size",
@@ -45,6 +48,7 @@ EXPORTS = ("dsa_workspace_size",
            "dsa_index_scores", "dsa_topk",
            "dsa_sparse_mla_fwd", "dsa_sparse_mla_fwd_ex", "dsa_sparse_mla_fwd_noalloc",
            "dsa_index_topk_attn", "dsa_index_topk_attn_ex",
+           "dsa_rope",
            "dsa_check_error", "dsa_check_error_noalloc", "dsa_set_wait_limit_ns",
            "dsa_launches_in_last_call", "dsa_launch_timing", "dsa_last_launch_times", "dsa_status_string")
 
@@ -75,6 +79,8 @@ _sig = {
     "dsa_index_topk_attn_ex": (ctypes.c_int, [_SEQ, _P, _P, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int,
                                               ctypes.c_int, ctypes.c_int, _F, _P, ctypes.c_int, _P, _P, _P, _SZ,
                                               ctypes.c_uint, _P, _P]),
+    "dsa_rope": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64, _I64, _I64, _I64,
+                                _P, _P, ctypes.c_int, ctypes.c_int, _F, ctypes.c_uint, _P]),
     "dsa_check_error": (ctypes.c_int, [_P, _P]),
     "dsa_check_error_noalloc": (ctypes.c_int, [_P]),
     "dsa_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
@@ -110,6 +116,24 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _on(device: torch.device):
+    """Makes `device` current for a launch, where another one is."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _NOTHING
+    return torch.cuda.device(device)
 
 
 def _need(t, name: str, dtypes, shape, device: torch.device, min_rows: int = 0):
@@ -424,6 +448,93 @@ def dsa_index_topk_attn(seqs: Seqs, qI, w, kI, kI_scale, q, kv, K: int, scale: f
                                        DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev, _stream(q.device)),
            "dsa_index_topk_attn")
     return out, lse
+
+
+_ROPE_DTYPES = {torch.bfloat16: DSA_ROPE_BF16, torch.float16: DSA_ROPE_F16, torch.float32: DSA_ROPE_F32}
+
+
+def _rope_view(t, name: str, dev: torch.device, dtype):
+    """[T, H, D] sizes and [T, H] strides of a [T, H, D] or [T, D] tensor
+    whose last dim is contiguous (the stride of a dim of one entry is 0)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    sz, st = t.shape, t.stride()
+    if len(sz) == 2:
+        T, H, D, a, b, last = sz[0], 1, sz[1], st[0], 0, st[1]
+    elif len(sz) == 3:
+        (T, H, D), (a, b, last) = sz, st
+    else:
+        raise ValueError(f"{name}: shape {list(sz)}, expected [T, H, D] or [T, D]")
+    if H < 1 or D < 1:
+        raise ValueError(f"{name}: shape {list(sz)} has no heads or no dims")
+    if last != 1 and D > 1:
+        raise ValueError(f"{name}: the last dim must be contiguous")
+    return T, H, D, a if T > 1 else 0, b if H > 1 else 0
+
+
+def _rope_disjoint(x, out, T, H, D, xt, xh, ot, oh) -> bool:
+    """x and out are one view, or share no element (two slices of the rows of
+    one buffer among them)."""
+    px, po, size = x.data_ptr(), out.data_ptr(), x.element_size()
+    if px == po and (xt, xh) == (ot, oh):
+        return True
+    if px + ((T - 1) * xt + (H - 1) * xh + D) * size <= po or po + ((T - 1) * ot + (H - 1) * oh + D) * size <= px:
+        return True
+    inner = oh if H > 1 else ot                     # the rows' pitch
+    if (xt, xh) != (ot, oh) or inner < D or (H > 1 and T > 1 and ot % oh):
+        return False
+    delta = (po - px) // size % inner
+    return (po - px) % size == 0 and D <= delta <= inner - D
+
+
+def dsa_rope(x: torch.Tensor, positions: torch.Tensor, table: RopeTable, offset: int = 0, out=None, transpose=False):
+    """Rotates dims offset .. offset + table.rot_dim - 1 of every row of x
+    ([T, H, D], or [T, D] for rows without heads; bf16, fp16 or fp32; any
+    strides over tokens and heads) by its token's position (int32 or int64
+    [T], negative ones too) and copies the other dims.
+
+    out: x itself (in place, the other dims untouched), a tensor or view of x's
+    shape that shares no element with x, or None for a new contiguous tensor.
+    transpose: the transposed map, which takes the gradient of the output to
+    that of x (with amplitude 1 it undoes the rotation).  The call records no
+    autograd graph and refuses an x that would need one."""
+    dev = _cuda_device(x, "x")
+    kind = _ROPE_DTYPES.get(x.dtype)
+    if kind is None:
+        raise TypeError(f"x: dtype {x.dtype}, expected one of {[str(d) for d in _ROPE_DTYPES]}")
+    if x.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("dsa_rope records no gradients: call it under torch.no_grad() and rotate the output's "
+                           "gradient with transpose=True")
+    T, H, D, xt, xh = _rope_view(x, "x", dev, x.dtype)
+    if not isinstance(table, RopeTable):
+        raise TypeError(f"table: expected a RopeTable, got {type(table).__name__}")
+    _need(table.turns, "table.turns", (torch.int64,), (table.rot_dim // 2,), dev)
+    _need(positions, "positions", (torch.int64, torch.int32), (T,), dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        ot, oh = H * D if T > 1 else 0, D if H > 1 else 0
+    else:
+        if out is x:
+            ot, oh = xt, xh
+        else:
+            ot, oh = _rope_view(out, "out", dev, x.dtype)[3:]
+            if out.shape != x.shape:
+                raise ValueError(f"out: shape {list(out.shape)}, expected {list(x.shape)}")
+            if out.requires_grad and torch.is_grad_enabled():
+                raise RuntimeError("out: dsa_rope records no gradients")
+        if T and not _rope_disjoint(x, out, T, H, D, xt, xh, ot, oh):
+            raise ValueError("x and out overlap without being the same view")
+    flags = (0 if table.interleaved else DSA_ROPE_HALF) | (DSA_ROPE_TRANSPOSE if transpose else 0) \
+        | (DSA_ROPE_POS64 if positions.dtype == torch.int64 else 0)
+    with _on(dev):
+        _check(_lib.dsa_rope(x.data_ptr(), out.data_ptr(), kind, T, H, D, xt, xh, ot, oh, positions.data_ptr(),
+                             table.turns.data_ptr(), table.rot_dim, offset, table.amplitude, flags, _stream(dev)),
+               "dsa_rope")
+    return out
 
 
 def dsa_check_error(ws: torch.Tensor) -> int:

@@ -364,6 +364,35 @@ dsa_status_t dsa_index_topk_attn(const dsa_seqs_t* seqs, const void* qI, const f
                                 out_dtype, lse, idx_out, ws, ws_bytes, 0u, nullptr, stream);
 }
 
+dsa_status_t dsa_rope(const void* x, void* out, int dtype, int T, int H, int D, int64_t x_stride_t, int64_t x_stride_h,
+                      int64_t out_stride_t, int64_t out_stride_h, const void* positions, const uint64_t* turns,
+                      int rot_dim, int offset, float amplitude, unsigned flags, dsa_stream_t stream) {
+  g_launches = 0;
+  if (dtype != DSA_ROPE_BF16 && dtype != DSA_ROPE_F16 && dtype != DSA_ROPE_F32) return DSA_ERR_UNSUPPORTED;
+  if (flags & ~(unsigned)(DSA_ROPE_HALF | DSA_ROPE_TRANSPOSE | DSA_ROPE_POS64)) return DSA_ERR_INVALID_ARG;
+  if (T < 0 || H < 1 || D < 1 || offset < 0 || rot_dim < 2 || rot_dim % 2) return DSA_ERR_INVALID_ARG;
+  if (rot_dim > (int)DSA_ROPE_MAX_DIM) return DSA_ERR_UNSUPPORTED;
+  if (offset > D - rot_dim || !std::isfinite(amplitude)) return DSA_ERR_INVALID_ARG;
+  if (T == 0) return DSA_OK;
+  const bool pos64 = flags & DSA_ROPE_POS64;
+  const size_t elem = dtype == DSA_ROPE_F32 ? 4 : 2;
+  if (!x || !out || !positions || !turns) return DSA_ERR_INVALID_ARG;
+  if (!aligned(x, elem) || !aligned(out, elem) || !aligned(positions, pos64 ? 8 : 4) || !aligned(turns, 8))
+    return DSA_ERR_INVALID_ARG;
+  // rows of out must not share elements: tokens outside heads, or heads outside tokens
+  const int64_t ot = out_stride_t, oh = out_stride_h;
+  if (x_stride_t < 0 || x_stride_h < 0 || ot < 0 || oh < 0) return DSA_ERR_INVALID_ARG;
+  const bool heads_in = (H == 1 || oh >= D) && (T == 1 || ot >= (H - 1) * oh + D);
+  const bool tokens_in = (T == 1 || ot >= D) && (H == 1 || oh >= (T - 1) * ot + D);
+  if (!heads_in && !tokens_in) return DSA_ERR_INVALID_ARG;
+  if (x == out && ((T > 1 && x_stride_t != ot) || (H > 1 && x_stride_h != oh))) return DSA_ERR_INVALID_ARG;
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_rope(RopeCall{x, out, dtype, T, H, D, x_stride_t, x_stride_h, ot, oh, positions, turns,
+                                          amplitude, rot_dim, offset, pos64, (flags & DSA_ROPE_HALF) != 0,
+                                          (flags & DSA_ROPE_TRANSPOSE) != 0},
+                                 (cudaStream_t)stream));
+}
+
 dsa_status_t dsa_check_error(void* ws, dsa_stream_t stream) {
   if (!ws) return DSA_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;

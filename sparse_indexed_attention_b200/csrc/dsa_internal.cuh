@@ -221,4 +221,18 @@ cudaError_t launch_sparse_mla(const SeqsDev& s, TokenMap tm, bool tm_early, cons
                               const uint8_t* kv8_scale, const int32_t* idx, int K, int H, float scale, void* out,
                               bool out_f32, float* lse, void* partials, uint32_t* err, cudaStream_t st);
 
+// Rotary positions (arguments checked by dsa_rope; strides in elements).
+struct RopeCall {
+  const void* x;
+  void* out;
+  int dtype, T, H, D;
+  int64_t xt, xh, ot, oh;
+  const void* pos;
+  const uint64_t* turns;
+  float amp;
+  int rot, offset;
+  bool pos64, half_layout, transpose;
+};
+cudaError_t launch_rope(const RopeCall& r, cudaStream_t st);
+
 }  // namespace dsa
