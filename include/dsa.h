@@ -38,8 +38,9 @@
  * Paged pools.  Logical position s of sequence b lives in physical row
  *   page_table[b*max_pages + s/64]*64 + s%64 of each pool (page size 64).
  *   Pools: index keys kI [R, 128] (bf16; FP8 E4M3 codes with one fp32 scale
- *   per row in kI_scale [R]; or MXFP8: E4M3 codes with one E8M0 scale byte
- *   per 32 elements in kI_scale [R, 4]) and latent KV [R, 576] (bf16; or
+ *   per row in kI_scale [R]; MXFP8: E4M3 codes with one E8M0 scale byte per 32
+ *   elements in kI_scale [R, 4]; or MXFP4: packed E2M1 codes [R, 64] with the
+ *   same scales) and latent KV [R, 576] (bf16; or
  *   E4M3 codes with five power-of-two tile-scale bytes per row in
  *   kv_scale [R, 8], see dsa_kv_dtype_t), R = num_phys_pages*64.
  * Fixed sizes.  Index heads H_I = 64, index dim d_I = 128, latent dims
@@ -96,10 +97,13 @@ typedef enum {
 typedef enum {
   DSA_KI_BF16 = 0,     /* kI pool is bf16 [R,128]; kI_scale must be NULL         */
   DSA_KI_FP8_E4M3 = 1, /* kI pool is OCP E4M3 codes [R,128] + fp32 kI_scale [R] */
-  DSA_KI_MXFP8 = 2     /* kI pool is OCP E4M3 codes [R,128] + E8M0 kI_scale
+  DSA_KI_MXFP8 = 2,    /* kI pool is OCP E4M3 codes [R,128] + E8M0 kI_scale
                           uint8 [R,4]: byte g scales elements 32g..32g+31 by
                           2^(byte - 127) ([P2] section 5 table, "Indexer Q/K":
                           MXFP8, one shared scale per group of 32; [P4] 4.2) */
+  DSA_KI_MXFP4 = 3     /* the same groups with 4-bit elements: kI pool is packed
+                          OCP E2M1 codes [R,64] (element 2i in the low half of
+                          byte i) + E8M0 kI_scale uint8 [R,4]; half MXFP8's bytes */
 } dsa_ki_dtype_t;
 
 typedef enum {
@@ -123,7 +127,8 @@ typedef enum {
   DSA_OP_TOPK = 2,
   DSA_OP_SPARSE_MLA = 3,
   DSA_OP_INDEX_TOPK_ATTN = 4,
-  DSA_OP_INDEX_TOPK_ATTN_FUSED = 5  /* dsa_index_topk_attn_ex with DSA_SELECT_IN_INDEXER */
+  DSA_OP_INDEX_TOPK_ATTN_FUSED = 5, /* dsa_index_topk_attn_ex with DSA_SELECT_IN_INDEXER */
+  DSA_OP_APPEND_INDEX_KEYS = 6
 } dsa_op_t;
 
 /* Flags of dsa_index_topk_attn_ex. */
@@ -208,6 +213,35 @@ dsa_status_t dsa_quantize_index_query(const void *qI, const float *w, int T,
 dsa_status_t dsa_quantize_index_query_mx(const void *qI, int T, uint8_t *codes,
                                          uint8_t *scales, dsa_stream_t stream);
 
+/* MXFP4 index-query quantization (the query side of DSA_KI_MXFP4): as
+ * dsa_quantize_index_query_mx with E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * a sign in bit 3).  For every group of 32: e = floor(log2(max |group|)) - 2
+ * clamped to [-127, 127] (e = 0 for an all-zero group); scale byte e + 127;
+ * codes = E2M1(group / 2^e) rounded to nearest-even with saturation at 6.  A
+ * group holding an infinity or NaN takes scale byte 255 (E8M0's NaN), codes 0.
+ *   qI bf16 [T,64,128]; codes uint8 [T,64,64] (out), two per byte, element 2i in
+ *   the low half of byte i; scales uint8 [T,64,4] (out).  No workspace. */
+dsa_status_t dsa_quantize_index_query_mx4(const void *qI, int T, uint8_t *codes,
+                                          uint8_t *scales, dsa_stream_t stream);
+
+/* Writes the batch's new index keys into an MXFP4 cache: row t of k (bf16
+ * [T,128]) is quantized as a query row is and stored in the pool row of token
+ * t's own position (positions ctx_len - q_len .. ctx_len - 1 of its sequence),
+ * codes to kI [R,64] and scales to kI_scale [R,4].  No other row is touched.
+ * Two tokens whose positions share a pool row (a page in two sequences' tables)
+ * must not be written by one call.  Workspace: DSA_OP_APPEND_INDEX_KEYS (the
+ * error word).  Invalid tokens and page ids are skipped (DSA_ERR_BAD_INDEX). */
+dsa_status_t dsa_append_index_keys_mx4(const dsa_seqs_t *seqs, const void *k,
+                                       uint8_t *kI, uint8_t *kI_scale, void *ws,
+                                       size_t ws_bytes, dsa_stream_t stream);
+
+/* MXFP4 rows back to bf16: out[r, 32g .. 32g+31] = E2M1(codes) * 2^(scales[r,g] -
+ * 127), exact (magnitudes above bf16's range give infinity, scale byte 255 gives
+ * NaN).  codes uint8 [rows,64], scales uint8 [rows,4], out bf16 [rows,128];
+ * rows at most 2^31 - 1.  No workspace. */
+dsa_status_t dsa_dequantize_mx4(const uint8_t *codes, const uint8_t *scales,
+                                int64_t rows, void *out, dsa_stream_t stream);
+
 /* Lightweight-indexer scores ([P2] section 2 item 2 and section 4(1); [P3]
  * sections 1 and 3 `fused_lightning_indexer`; [P4] section 3.1): for every
  * query token t and candidate s = 0..pos(t),
@@ -216,11 +250,12 @@ dsa_status_t dsa_quantize_index_query_mx(const void *qI, int T, uint8_t *codes,
  * in dsa_quantize_index_query (the scores are those of the quantized qI).
  * MXFP8 cache: kI[s,32g..32g+31] = E4M3(codes) * 2^(kI_scale[s,g] - 127) and qI
  * is first quantized as in dsa_quantize_index_query_mx; the group scales are
- * applied by the tensor core's block-scaled MMA.
+ * applied by the tensor core's block-scaled MMA.  MXFP4 cache: likewise with E2M1
+ * codes and dsa_quantize_index_query_mx4.
  * Entries s > pos(t) of a row are left untouched.  ld >= max_ctx.
  * The reduction over heads happens in the kernel; no [T,H_I,N] tensor exists.
  *   qI bf16 [T,64,128]; w fp32 [T,64]; kI pool; kI_scale fp32 [R], uint8
- *   [R,4] (MXFP8) or NULL (bf16); scores fp32 [T,ld] (out). */
+ *   [R,4] (MXFP8, MXFP4) or NULL (bf16); scores fp32 [T,ld] (out). */
 dsa_status_t dsa_index_scores(const dsa_seqs_t *seqs, const void *qI,
                               const float *w, const void *kI,
                               const void *kI_scale, dsa_ki_dtype_t ki_dtype,

@@ -32,19 +32,20 @@ LIB_PATH = _build.LIB
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_BAD_INDEX, \
     DSA_ERR_TIMEOUT = range(7)
-DSA_KI_BF16, DSA_KI_FP8_E4M3, DSA_KI_MXFP8 = 0, 1, 2
+DSA_KI_BF16, DSA_KI_FP8_E4M3, DSA_KI_MXFP8, DSA_KI_MXFP4 = range(4)
 DSA_KV_BF16, DSA_KV_FP8_E4M3 = 0, 1
 DSA_OUT_BF16, DSA_OUT_F32 = 0, 1
 DSA_NOALLOC_SCRATCH_BYTES = 32 << 20
 DSA_OP_QUANTIZE_INDEX_QUERY, DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_INDEX_TOPK_ATTN, \
-    DSA_OP_INDEX_TOPK_ATTN_FUSED = range(6)
+    DSA_OP_INDEX_TOPK_ATTN_FUSED, DSA_OP_APPEND_INDEX_KEYS = range(7)
 DSA_SELECT_IN_INDEXER = 1
 DSA_ROPE_BF16, DSA_ROPE_F16, DSA_ROPE_F32 = range(3)
 DSA_ROPE_HALF, DSA_ROPE_TRANSPOSE, DSA_ROPE_POS64, DSA_ROPE_MAX_DIM = 1, 2, 4, 1024
 
 # Names the C header declares (checked against include/dsa.h by the tests).
 EXPORTS = ("dsa_workspace_size",
-           "dsa_quantize_index_query", "dsa_quantize_index_query_mx",
+           "dsa_quantize_index_query", "dsa_quantize_index_query_mx", "dsa_quantize_index_query_mx4",
+           "dsa_append_index_keys_mx4", "dsa_dequantize_mx4",
            "dsa_index_scores", "dsa_topk",
            "dsa_sparse_mla_fwd", "dsa_sparse_mla_fwd_ex", "dsa_sparse_mla_fwd_noalloc",
            "dsa_index_topk_attn", "dsa_index_topk_attn_ex",
@@ -66,6 +67,9 @@ _sig = {
     "dsa_workspace_size": (_SZ, [ctypes.c_int, _SEQ, ctypes.c_int, ctypes.c_int]),
     "dsa_quantize_index_query": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _P]),
     "dsa_quantize_index_query_mx": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P]),
+    "dsa_quantize_index_query_mx4": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P]),
+    "dsa_append_index_keys_mx4": (ctypes.c_int, [_SEQ, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_dequantize_mx4": (ctypes.c_int, [_P, _P, _I64, _P, _P]),
     "dsa_index_scores": (ctypes.c_int, [_SEQ, _P, _P, _P, _P, ctypes.c_int, _P, _I64, _P, _SZ, _P]),
     "dsa_topk": (ctypes.c_int, [_P, _I64, ctypes.c_int, _P, ctypes.c_int, _P, _P, _SZ, _P]),
     "dsa_sparse_mla_fwd": (ctypes.c_int, [_SEQ, _P, _P, _P, ctypes.c_int, ctypes.c_int, _F, _P, ctypes.c_int, _P, _P,
@@ -179,7 +183,7 @@ def _cuda_device(t, name: str) -> torch.device:
 
 
 _I32T, _F32T, _BF16T = (torch.int32,), (torch.float32,), (torch.bfloat16,)
-_FP8T = (torch.uint8, torch.float8_e4m3fn)
+_FP8T, _U8T = (torch.uint8, torch.float8_e4m3fn), (torch.uint8,)
 
 
 def _need_seqs(seqs: "Seqs", dev: torch.device):
@@ -199,22 +203,32 @@ def _need_index_inputs(seqs: "Seqs", qI, w, kI, kI_scale, check_seqs: bool = Tru
         _need_seqs(seqs, dev)
     _need(qI, "qI", _BF16T, (T, 64, 128), dev)
     _need(w, "w", _F32T, (T, 64), dev)
-    _need(kI, "kI", _FP8T if kI_scale is not None else _BF16T, (None, 128), dev, rows)
+    if _is_mx4(kI, kI_scale):
+        _need(kI, "kI", _U8T, (None, 64), dev, rows)
+    else:
+        _need(kI, "kI", _FP8T if kI_scale is not None else _BF16T, (None, 128), dev, rows)
     if _is_mx(kI_scale):
-        _need(kI_scale, "kI_scale", (torch.uint8,), (None, 4), dev, rows)
+        _need(kI_scale, "kI_scale", _U8T, (None, 4), dev, rows)
     elif kI_scale is not None:
         _need(kI_scale, "kI_scale", _F32T, (None,), dev, rows)
     return dev
 
 
 def _is_mx(kI_scale) -> bool:
-    """An MXFP8 index cache carries E8M0 group scales (uint8 [R, 4])."""
+    """An MXFP8 or MXFP4 index cache carries E8M0 group scales (uint8 [R, 4])."""
     return kI_scale is not None and kI_scale.dtype == torch.uint8
 
 
-def _ki_dtype(kI_scale) -> int:
+def _is_mx4(kI, kI_scale) -> bool:
+    """Rows of 64 bytes with group scales hold packed 4-bit codes."""
+    return _is_mx(kI_scale) and isinstance(kI, torch.Tensor) and kI.dim() == 2 and kI.shape[1] == 64
+
+
+def _ki_dtype(kI_scale, kI=None) -> int:
     if kI_scale is None:
         return DSA_KI_BF16
+    if _is_mx4(kI, kI_scale):
+        return DSA_KI_MXFP4
     return DSA_KI_MXFP8 if _is_mx(kI_scale) else DSA_KI_FP8_E4M3
 
 
@@ -327,8 +341,60 @@ def dsa_quantize_index_query_mx(qI: torch.Tensor, codes=None, scales=None):
     return codes, scales
 
 
+def dsa_quantize_index_query_mx4(qI: torch.Tensor, codes=None, scales=None):
+    """MXFP4: qI [T, 64, 128] bf16 to packed E2M1 codes uint8 [T, 64, 64] and
+    E8M0 scales uint8 [T, 64, 4]."""
+    dev = _cuda_device(qI, "qI")
+    T = qI.shape[0]
+    codes = codes if codes is not None else torch.empty((T, 64, 64), dtype=torch.uint8, device=dev)
+    scales = scales if scales is not None else torch.empty((T, 64, 4), dtype=torch.uint8, device=dev)
+    _need(qI, "qI", _BF16T, (T, 64, 128), dev)
+    _need(codes, "codes", _U8T, (T, 64, 64), dev)
+    _need(scales, "scales", _U8T, (T, 64, 4), dev)
+    with _on(dev):
+        _check(_lib.dsa_quantize_index_query_mx4(_ptr(qI), T, _ptr(codes), _ptr(scales), _stream(dev)),
+               "dsa_quantize_index_query_mx4")
+    return codes, scales
+
+
+def dsa_append_index_keys_mx4(seqs: Seqs, k: torch.Tensor, kI: torch.Tensor, kI_scale: torch.Tensor, ws=None):
+    """Quantizes the new tokens' index keys k [T, 128] bf16 into the rows of
+    their positions of an MXFP4 cache: kI uint8 [R, 64], kI_scale uint8 [R, 4]."""
+    dev = _cuda_device(k, "k")
+    _need_seqs(seqs, dev)
+    _need(k, "k", _BF16T, (seqs.num_q_tokens, 128), dev)
+    rows = seqs.num_phys_pages * 64
+    _need(kI, "kI", _U8T, (None, 64), dev, rows)
+    _need(kI_scale, "kI_scale", _U8T, (None, 4), dev, rows)
+    c = seqs.c()
+    ws = ws if ws is not None else workspace(256, dev, "append_index_keys")
+    _need_ws(ws, dev)
+    with _on(dev):
+        _check(_lib.dsa_append_index_keys_mx4(ctypes.byref(c), _ptr(k), _ptr(kI), _ptr(kI_scale), _ptr(ws),
+                                              ws.numel(), _stream(dev)), "dsa_append_index_keys_mx4")
+
+
+def dsa_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None) -> torch.Tensor:
+    """The bf16 values [..., 128] that MXFP4 codes [..., 64] with scales [..., 4]
+    stand for (exact)."""
+    dev = _cuda_device(codes, "codes")
+    if codes.dim() < 1 or codes.shape[-1] != 64:
+        raise ValueError(f"codes: shape {list(codes.shape)}, expected [..., 64]")
+    lead = tuple(codes.shape[:-1])
+    out = out if out is not None else torch.empty((*lead, 128), dtype=torch.bfloat16, device=dev)
+    _need(codes, "codes", _U8T, (*lead, 64), dev)
+    _need(scales, "scales", _U8T, (*lead, 4), dev)
+    _need(out, "out", _BF16T, (*lead, 128), dev)
+    with _on(dev):
+        _check(_lib.dsa_dequantize_mx4(_ptr(codes), _ptr(scales), codes.numel() // 64, _ptr(out), _stream(dev)),
+               "dsa_dequantize_mx4")
+    return out
+
+
 def dsa_index_scores(seqs: Seqs, qI, w, kI, kI_scale=None, scores=None, ld=None, ws=None):
-    """Scores into `scores` [T, ld] fp32 (allocated zeroed when None).  When
+    """Scores into `scores` [T, ld] fp32 (allocated zeroed when None).  The index
+    cache's format follows kI and kI_scale: bf16 [R, 128] without scales; E4M3
+    [R, 128] with fp32 [R]; MXFP8 [R, 128] or MXFP4 [R, 64] with uint8 [R, 4].  When
     `scores` is given, ld defaults to its row stride and must equal it."""
     dev = _need_index_inputs(seqs, qI, w, kI, kI_scale)
     T = seqs.num_q_tokens
@@ -340,7 +406,7 @@ def dsa_index_scores(seqs: Seqs, qI, w, kI, kI_scale=None, scores=None, ld=None,
         if ld is not None and ld != scores.stride(0):
             raise ValueError(f"ld={ld} differs from the row stride {scores.stride(0)} of scores")
         ld = scores.stride(0)
-    ki_dtype = _ki_dtype(kI_scale)
+    ki_dtype = _ki_dtype(kI_scale, kI)
     c = seqs.c()
     need = _lib.dsa_workspace_size(DSA_OP_INDEX_SCORES, ctypes.byref(c), 1, 16)
     ws = ws if ws is not None else workspace(need, qI.device, "index_scores")
@@ -434,7 +500,7 @@ def dsa_index_topk_attn(seqs: Seqs, qI, w, kI, kI_scale, q, kv, K: int, scale: f
         raise ValueError("qI and q are on different devices")
     if idx_out is not None:
         _need(idx_out, "idx_out", _I32T, (T, K), dev)
-    ki_dtype = _ki_dtype(kI_scale)
+    ki_dtype = _ki_dtype(kI_scale, kI)
     c = seqs.c()
     op = DSA_OP_INDEX_TOPK_ATTN_FUSED if select_in_indexer else DSA_OP_INDEX_TOPK_ATTN
     need = _lib.dsa_workspace_size(op, ctypes.byref(c), K, H)

@@ -59,7 +59,7 @@ Layout make_layout(dsa_op_t op, int T, int B, int max_ctx, int K, int H) {
     L.items = take((size_t)plan_max_items(T, B, max_ctx, tg) * 2 * sizeof(int4));
     L.q_codes = take((size_t)T * kHI * kDI);
     L.w_scaled = take((size_t)T * kHI * sizeof(float));
-    L.q_sf = take((size_t)T * kHI * 4);  // MXFP8 query group scales (E8M0)
+    L.q_sf = take((size_t)T * kHI * 4);  // MXFP8 / MXFP4 query group scales (E8M0)
   }
   if (op == DSA_OP_INDEX_TOPK_ATTN) {
     L.ld = ((int64_t)max_ctx + 3) / 4 * 4;
@@ -130,7 +130,8 @@ dsa_status_t check_indexer_args(const dsa_seqs_t* seqs, const void* qI, const fl
                                 const void* kI_scale, dsa_ki_dtype_t ki_dtype) {
   DSA_TRY(check_seqs(seqs));
   if (!qI || !w || !kI) return DSA_ERR_INVALID_ARG;
-  if (ki_dtype != DSA_KI_BF16 && ki_dtype != DSA_KI_FP8_E4M3 && ki_dtype != DSA_KI_MXFP8) return DSA_ERR_UNSUPPORTED;
+  if (ki_dtype != DSA_KI_BF16 && ki_dtype != DSA_KI_FP8_E4M3 && ki_dtype != DSA_KI_MXFP8 && ki_dtype != DSA_KI_MXFP4)
+    return DSA_ERR_UNSUPPORTED;
   if ((ki_dtype != DSA_KI_BF16) != (kI_scale != nullptr)) return DSA_ERR_INVALID_ARG;
   if (!aligned(qI, 16) || !aligned(w, 16) || !aligned(kI, 128) || (kI_scale && !aligned(kI_scale, 16)))
     return DSA_ERR_INVALID_ARG;
@@ -167,21 +168,22 @@ PlanBufs plan_bufs(void* ws, const Layout& L) {
   return p;
 }
 
-// Tokens per indexer group for a call: one for decode, else two (bf16 and
-// MXFP8 caches) or four (E4M3 cache).
+// Tokens per indexer group for a call: one for decode, else two (bf16, MXFP8
+// and MXFP4 caches) or four (E4M3 cache).
 int group_tokens(const dsa_seqs_t* seqs, dsa_ki_dtype_t ki_dtype) {
   return indexer_group_tokens(seqs->num_q_tokens, seqs->batch, ki_dtype == DSA_KI_FP8_E4M3);
 }
 
 // Indexer launch sequence shared by dsa_index_scores and the fused call: one
-// prep launch (plan, FP8 / MXFP8 query quantization, zeroing of `zero`) and
+// prep launch (plan, FP8 / MXFP8 / MXFP4 query quantization, zeroing of `zero`) and
 // the indexer, which also accumulates Top-K's first-digit histogram into
 // `hist` when that is given (one token per group).
 dsa_status_t run_indexer(const dsa_seqs_t* seqs, const SeqsDev& sd, const PlanBufs& plan, int tg, const void* qI,
                          const float* w, const void* kI, const void* kI_scale, dsa_ki_dtype_t ki_dtype,
                          float* scores, int64_t ld, void* ws, const Layout& L, uint32_t* hist, uint32_t* zero,
                          int64_t zero_words, uint32_t* err, cudaStream_t st, const FusedTopk* fused = nullptr) {
-  const bool fp8 = ki_dtype == DSA_KI_FP8_E4M3, mx = ki_dtype == DSA_KI_MXFP8;
+  const bool fp8 = ki_dtype == DSA_KI_FP8_E4M3, mx4 = ki_dtype == DSA_KI_MXFP4;
+  const bool mx = mx4 || ki_dtype == DSA_KI_MXFP8;
   const void* q_operand = qI;
   const float* w_operand = w;
   uint8_t* codes = (fp8 || mx) ? at<uint8_t>(ws, L.q_codes) : nullptr;
@@ -189,14 +191,14 @@ dsa_status_t run_indexer(const dsa_seqs_t* seqs, const SeqsDev& sd, const PlanBu
   uint8_t* q_sf = mx ? at<uint8_t>(ws, L.q_sf) : nullptr;
   DSA_CUDA(launch_prep(sd, tg, indexer_item_tiles(tg), plan,
                        (fp8 || mx) ? reinterpret_cast<const __nv_bfloat16*>(qI) : nullptr, w, codes, w_scaled, q_sf,
-                       zero, zero_words, err, st));
+                       mx4, zero, zero_words, err, st));
   if (fp8) {
     q_operand = codes;
     w_operand = w_scaled;
   } else if (mx) {
     q_operand = codes;  // the head weights stay as given: the group scales ride in the MMA
   }
-  const IdxFmt fmt = mx ? IdxFmt::kMx : (fp8 ? IdxFmt::kE4M3 : IdxFmt::kBf16);
+  const IdxFmt fmt = mx4 ? IdxFmt::kMx4 : mx ? IdxFmt::kMx : (fp8 ? IdxFmt::kE4M3 : IdxFmt::kBf16);
   DSA_CUDA(launch_index_scores(sd, plan, tg, q_operand, w_operand, q_sf, kI, kI_scale, fmt, scores, ld, hist, err, st,
                                fused));
   return DSA_OK;
@@ -210,7 +212,7 @@ size_t dsa_workspace_size(dsa_op_t op, const dsa_seqs_t* seqs, int K, int H) {
   if (!seqs || seqs->num_q_tokens < 1 || seqs->max_ctx < 1) return 0;
   if (op == DSA_OP_QUANTIZE_INDEX_QUERY) return 0;
   if (op == DSA_OP_TOPK) return make_layout(op, seqs->num_q_tokens, 1, seqs->max_ctx, K, 16).total;
-  if (op < 0 || op > DSA_OP_INDEX_TOPK_ATTN_FUSED) return 0;
+  if (op < 0 || op > DSA_OP_APPEND_INDEX_KEYS) return 0;
   if (seqs->batch < 1) return 0;
   if ((op == DSA_OP_SPARSE_MLA || op == DSA_OP_INDEX_TOPK_ATTN || op == DSA_OP_INDEX_TOPK_ATTN_FUSED) &&
       (K < 1 || K > kMaxK || !valid_H(H)))
@@ -237,6 +239,39 @@ dsa_status_t dsa_quantize_index_query_mx(const void* qI, int T, uint8_t* codes, 
   timer_begin((cudaStream_t)stream);
   return cuda_status(launch_quantize_index_query_mx(reinterpret_cast<const __nv_bfloat16*>(qI), T, codes, scales,
                                                     (cudaStream_t)stream));
+}
+
+dsa_status_t dsa_quantize_index_query_mx4(const void* qI, int T, uint8_t* codes, uint8_t* scales,
+                                          dsa_stream_t stream) {
+  g_launches = 0;
+  if (!qI || !codes || !scales || T < 1) return DSA_ERR_INVALID_ARG;
+  if (!aligned(qI, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return DSA_ERR_INVALID_ARG;
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_quantize_index_query_mx4(reinterpret_cast<const __nv_bfloat16*>(qI), T, codes, scales,
+                                                     (cudaStream_t)stream));
+}
+
+dsa_status_t dsa_append_index_keys_mx4(const dsa_seqs_t* seqs, const void* k, uint8_t* kI, uint8_t* kI_scale, void* ws,
+                                       size_t ws_bytes, dsa_stream_t stream) {
+  g_launches = 0;
+  DSA_TRY(check_seqs(seqs));
+  if (!k || !kI || !kI_scale) return DSA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(kI, 128) || !aligned(kI_scale, 16)) return DSA_ERR_INVALID_ARG;
+  DSA_TRY(check_ws(ws, ws_bytes, kAlign));
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_append_index_keys_mx4(to_dev(seqs), reinterpret_cast<const __nv_bfloat16*>(k), kI,
+                                                  kI_scale, at<uint32_t>(ws, 0), (cudaStream_t)stream));
+}
+
+dsa_status_t dsa_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, void* out,
+                                dsa_stream_t stream) {
+  g_launches = 0;
+  if (!codes || !scales || !out || rows < 1) return DSA_ERR_INVALID_ARG;
+  if (rows > (int64_t)INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_dequantize_mx4(codes, scales, rows, reinterpret_cast<__nv_bfloat16*>(out),
+                                           (cudaStream_t)stream));
 }
 
 dsa_status_t dsa_index_scores(const dsa_seqs_t* seqs, const void* qI, const float* w, const void* kI,

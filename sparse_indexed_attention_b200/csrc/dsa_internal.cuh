@@ -75,6 +75,33 @@ struct SeqsDev {
   const int32_t* page_table;
 };
 
+// Sequence and absolute position of query token t; pos -1 for a token that
+// belongs to no valid sequence (the planner's rule: the sequence's query rows
+// lie inside the T rows and its lengths and pages inside their bounds).
+struct TokenPlace {
+  int seq, pos, q_len;
+};
+__device__ __forceinline__ TokenPlace locate_token(const SeqsDev& s, int t) {
+  // decode batches hold one token per sequence: try sequence t before a search
+  int b = t < s.batch ? t : s.batch - 1;
+  int lo_start = __ldg(s.q_seq_start + b), hi_start = __ldg(s.q_seq_start + b + 1);
+  if (t < lo_start || t >= hi_start) {
+    int lo = 0, hi = s.batch - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(s.q_seq_start + mid) <= t) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    lo_start = __ldg(s.q_seq_start + b);
+    hi_start = __ldg(s.q_seq_start + b + 1);
+  }
+  const int q_len = hi_start - lo_start, ctx = __ldg(s.ctx_len + b);
+  const bool ok = __ldg(s.q_seq_start) == 0 && lo_start >= 0 && hi_start <= s.num_tokens && t >= lo_start &&
+                  t < hi_start && ctx >= 1 && ctx <= s.max_ctx && q_len <= ctx &&
+                  (ctx + kPage - 1) / kPage <= s.max_pages;
+  return {b, ok ? ctx - q_len + (t - lo_start) : -1, q_len};
+}
+
 // Programmatic dependent launch: every kernel of the path is launched with
 // programmatic stream serialization, so its launch and its set-up (barrier
 // init, TMEM allocation, tensor-map prefetch) overlap the previous kernel's
@@ -168,11 +195,11 @@ inline int64_t plan_max_items(int T, int B, int max_ctx, int tg) {
 
 // ---- launchers (each returns cudaGetLastError() of its launch) ----
 cudaError_t launch_plan(const SeqsDev& s, int tg, int ch, const PlanBufs& p, uint32_t* err, cudaStream_t st);
-// Plan + (FP8 / MXFP8 cache: qI quantization) + zeroing of `zero_words` words,
-// one launch.  q_sf non-null selects MXFP8: the E8M0 group scales go to
-// q_sf [T*64, 4].
+// Plan + (FP8 / MXFP8 / MXFP4 cache: qI quantization) + zeroing of `zero_words` words,
+// one launch.  q_sf non-null selects MXFP8, or MXFP4 with mx4 set: the E8M0
+// group scales go to q_sf [T*64, 4].
 cudaError_t launch_prep(const SeqsDev& s, int tg, int ch, const PlanBufs& plan, const __nv_bfloat16* qI,
-                        const float* w, uint8_t* codes, float* w_scaled, uint8_t* q_sf, uint32_t* zero,
+                        const float* w, uint8_t* codes, float* w_scaled, uint8_t* q_sf, bool mx4, uint32_t* zero,
                         int64_t zero_words, uint32_t* err, cudaStream_t st);
 cudaError_t launch_quantize_index_query(const __nv_bfloat16* qI, const float* w, int T, uint8_t* codes,
                                         float* w_scaled, cudaStream_t st);
@@ -195,10 +222,10 @@ bool indexer_fused_fits(int T, int B, int max_ctx);    // the geometry fits the 
 int64_t fused_topk_words(int T, int B, int max_ctx);   // its zeroed scratch, in 32-bit words
 size_t fused_topk_cand_bytes(int T);                   // its candidate lists
 // Index-cache formats of the indexer kernel.
-enum class IdxFmt { kBf16, kE4M3, kMx };
+enum class IdxFmt { kBf16, kE4M3, kMx, kMx4 };
 // E4M3 cache: codes/w_scaled from the quantizer, kI_scale fp32 [R];
-// MXFP8 cache: codes and q_sf (E8M0 group scales) from the quantizer, w
-// directly, kI_scale E8M0 bytes [R, 4]; bf16 cache: qI/w directly.
+// MXFP8 and MXFP4 caches: codes and q_sf (E8M0 group scales) from the
+// quantizer, w directly, kI_scale E8M0 bytes [R, 4]; bf16 cache: qI/w directly.
 // hist (may be null; used for one token per group): Top-K first-digit histogram to accumulate into.
 // fused (may be null): select the Top-K in the same kernel instead of writing scores.
 cudaError_t launch_index_scores(const SeqsDev& s, const PlanBufs& plan, int tg, const void* q_operand,
@@ -220,6 +247,14 @@ size_t sparse_mla_partials_bytes(int T, int K, int H);
 cudaError_t launch_sparse_mla(const SeqsDev& s, TokenMap tm, bool tm_early, const __nv_bfloat16* q, const void* kv,
                               const uint8_t* kv8_scale, const int32_t* idx, int K, int H, float scale, void* out,
                               bool out_f32, float* lse, void* partials, uint32_t* err, cudaStream_t st);
+
+// MXFP4 index cache (k_mx4.cu).
+cudaError_t launch_quantize_index_query_mx4(const __nv_bfloat16* qI, int T, uint8_t* codes, uint8_t* scales,
+                                            cudaStream_t st);
+cudaError_t launch_append_index_keys_mx4(const SeqsDev& s, const __nv_bfloat16* k, uint8_t* codes, uint8_t* scales,
+                                         uint32_t* err, cudaStream_t st);
+cudaError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, __nv_bfloat16* out,
+                                  cudaStream_t st);
 
 // Rotary positions (arguments checked by dsa_rope; strides in elements).
 struct RopeCall {

@@ -25,6 +25,9 @@
 //    the MMA lane moves them into TMEM with tcgen05.cp (32 rows x 128 bits,
 //    written to every lane quarter) ahead of the tile's MMAs.  The epilogue
 //    is that of the E4M3 cache without the key scale.
+//  * MXFP4 cache: the same with packed E2M1 codes, rows of 64 bytes in the
+//    64-byte swizzle, and kind::mxf4 (two MMAs of 64 dims per tile): half the
+//    bytes of a key and twice the tensor rate.
 //  * warp 2: allocates and frees TMEM.
 //  * warps 4-11: epilogue, two warpgroups taking alternate tiles.  Thread r
 //    of a warpgroup owns TMEM lane r = key row r, so the ReLU, the head
@@ -85,15 +88,18 @@ struct TailSmem {
   int fast[kTailRuns];           // the row takes the candidate-list path
 };
 
-template <bool kBf16, int TG, bool kFused = false, bool kMx = false>
+// kMx4 (with kMx): the MXFP4 cache, packed E2M1 rows of 64 bytes.
+template <bool kBf16, int TG, bool kFused = false, bool kMx = false, bool kMx4 = false>
 struct IdxCfg {
   static_assert(!kFused || TG == 1, "the fused selection serves one token per group");
-  static_assert(!kMx || (!kBf16 && TG <= 2), "MXFP8: E4M3 codes, at most two tokens per group");
+  static_assert(!kMx || (!kBf16 && TG <= 2), "MXFP8, MXFP4: at most two tokens per group");
+  static_assert(kMx || !kMx4, "MXFP4 is an MX cache");
   static constexpr int N = 64 * TG;                        // MMA N: heads x tokens of a group
-  static constexpr int A_BYTES = kBf16 ? 32768 : 16384;    // 128 keys x d_I
-  static constexpr int B_BYTES = kBf16 ? N * 256 : N * 128;
+  static constexpr int ROW = kBf16 ? 256 : (kMx4 ? 64 : 128);  // bytes of an operand row
+  static constexpr int A_BYTES = 128 * ROW;                // 128 keys x d_I
+  static constexpr int B_BYTES = N * ROW;
   static constexpr int KSTEPS = kBf16 ? 8 : 4;             // 32-byte K steps per tile
-  static constexpr int NS = kBf16 ? 3 : (TG == 1 ? (kFused ? 6 : 8) : 6);
+  static constexpr int NS = kBf16 ? 3 : (kMx4 ? (kFused ? 8 : 12) : (TG == 1 ? (kFused ? 6 : 8) : 6));
   // Accumulator ring.  NACC is even: the two epilogue warpgroups take
   // alternate tiles, so each accumulator (and its barriers) belongs to one
   // warpgroup and is waited on one phase at a time.  MXFP8 also keeps scale
@@ -514,11 +520,11 @@ __device__ __forceinline__ void flush_hist(uint32_t* sh, uint32_t* gh, int t, in
   __syncwarp();
 }
 
-template <bool kBf16, int TG, bool kFused, bool kMx>
+template <bool kBf16, int TG, bool kFused, bool kMx, bool kMx4>
 __global__ void __launch_bounds__(kIdxThreads, 1)
 k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q,
                   const IdxArgs a) {
-  using C = IdxCfg<kBf16, TG, kFused, kMx>;
+  using C = IdxCfg<kBf16, TG, kFused, kMx, kMx4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -693,7 +699,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 tma_load_2d(adst + h * 8192, &tmap_k, &full[stage], 0, rows[h]);
                 tma_load_2d(adst + 16384 + h * 8192, &tmap_k, &full[stage], 64, rows[h]);
               } else {
-                tma_load_2d(adst + h * 8192, &tmap_k, &full[stage], 0, rows[h]);
+                tma_load_2d(adst + h * (C::A_BYTES / 2), &tmap_k, &full[stage], 0, rows[h]);
                 if constexpr (!kMx)
                   bulk_load(smem + C::OFF_SC + stage * 512 + h * 256, a.kI_scale + rows[h], 256, &full[stage]);
               }
@@ -760,15 +766,23 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           tc_fence_after();
           const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
           if constexpr (kMx) {
-            // the tile's key scales into TMEM, then one block-scaled MMA per
-            // 32-wide K block (byte k of each scale column)
+            // the tile's key scales into TMEM, then (MXFP8) one block-scaled MMA
+            // per 32-wide K block, byte k of each scale column
             fence_proxy_async_smem();  // written by cp.async (generic proxy)
             tmem_cp_32x128b_x4(tmem + C::SFA0 + 4 * stage, rows16_desc(smem_u32(smem + C::OFF_SC + stage * 512)));
+            if constexpr (kMx4) {  // one MMA per 64 of the 128 dims: bytes 0, 1 and 2, 3 of each scale column
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
-                     make_idesc_mx(128, C::N, k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)k << 30),
-                     (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+              for (int k = 0; k < 2; ++k)
+                mma_mx4(tmem + acc * C::N, sw64_kmajor_desc(a_base + k * 32), sw64_kmajor_desc(b_base + k * 32),
+                        make_idesc_mx4(128, C::N, 2 * k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)(2 * k) << 30),
+                        (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
+                       make_idesc_mx(128, C::N, k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)k << 30),
+                       (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+            }
           } else {
 #pragma unroll
             for (int k = 0; k < C::KSTEPS; ++k) {
@@ -929,9 +943,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Row-major 2-D map: rows of `row_elems` elements, box of box_x x box_y, 128-byte swizzle.
+// Row-major 2-D map: rows of `row_elems` elements, box of box_x x box_y,
+// 128-byte swizzle (64-byte for the 64-byte rows of MXFP4 codes).
 bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint32_t box_x,
               uint32_t box_y) {
+  const bool narrow = !bf16 && row_elems == 64;
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {row_elems, rows};
@@ -939,8 +955,9 @@ bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t row_elems, u
   const cuuint32_t box[2] = {box_x, box_y};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {
@@ -950,20 +967,20 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-template <bool kBf16, int TG, bool kFused, bool kMx = false>
+template <bool kBf16, int TG, bool kFused, bool kMx = false, bool kMx4 = false>
 cudaError_t launch_tc(const CUtensorMap& mk, const CUtensorMap& mq, const IdxArgs& a, int grid, cudaStream_t st) {
-  using C = IdxCfg<kBf16, TG, kFused, kMx>;
+  using C = IdxCfg<kBf16, TG, kFused, kMx, kMx4>;
   static thread_local int attr_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (attr_dev != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k_index_scores_tc<kBf16, TG, kFused, kMx>,
+    cudaError_t e = cudaFuncSetAttribute(k_index_scores_tc<kBf16, TG, kFused, kMx, kMx4>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_dev = dev;
   }
-  cudaError_t e = launch_pdl("index_scores", k_index_scores_tc<kBf16, TG, kFused, kMx>, dim3(grid), dim3(kIdxThreads),
-                             (size_t)C::SMEM, st, mk, mq, a);
+  cudaError_t e = launch_pdl("index_scores", k_index_scores_tc<kBf16, TG, kFused, kMx, kMx4>, dim3(grid),
+                             dim3(kIdxThreads), (size_t)C::SMEM, st, mk, mq, a);
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }
@@ -972,9 +989,9 @@ cudaError_t launch_tc(const CUtensorMap& mk, const CUtensorMap& mq, const IdxArg
 
 int indexer_fused_capacity() {
   const int a = IdxCfg<false, 1, true>::CAP_ITEMS, b = IdxCfg<true, 1, true>::CAP_ITEMS;
-  const int c = IdxCfg<false, 1, true, true>::CAP_ITEMS;
-  const int ab = a < b ? a : b;
-  return ab < c ? ab : c;
+  const int c = IdxCfg<false, 1, true, true>::CAP_ITEMS, d = IdxCfg<false, 1, true, true, true>::CAP_ITEMS;
+  const int ab = a < b ? a : b, cd = c < d ? c : d;
+  return ab < cd ? ab : cd;
 }
 
 bool indexer_fused_fits(int T, int B, int max_ctx) {
@@ -993,12 +1010,13 @@ cudaError_t launch_index_scores(const SeqsDev& s, const PlanBufs& plan, int tg, 
                                 const float* w_operand, const uint8_t* q_sf, const void* kI, const void* kI_scale,
                                 IdxFmt fmt, float* scores, int64_t ld, uint32_t* hist, uint32_t* err,
                                 cudaStream_t st, const FusedTopk* fused) {
-  const bool bf16 = fmt == IdxFmt::kBf16, mx = fmt == IdxFmt::kMx;
+  const bool bf16 = fmt == IdxFmt::kBf16, mx4 = fmt == IdxFmt::kMx4, mx = mx4 || fmt == IdxFmt::kMx;
   const uint64_t R = (uint64_t)s.num_phys_pages * kPage;
   const uint64_t qrows = (uint64_t)s.num_tokens * kHI;
   CUtensorMap mk, mq;
-  if (!make_map(&mk, kI, bf16, kDI, R, bf16 ? 64 : 128, 64)) return cudaErrorInvalidValue;
-  if (!make_map(&mq, q_operand, bf16, kDI, qrows, bf16 ? 64 : 128, 64 * tg)) return cudaErrorInvalidValue;
+  const int row = mx4 ? kDI / 2 : kDI;  // elements (bytes of codes) per row
+  if (!make_map(&mk, kI, bf16, row, R, bf16 ? 64 : row, 64)) return cudaErrorInvalidValue;
+  if (!make_map(&mq, q_operand, bf16, row, qrows, bf16 ? 64 : row, 64 * tg)) return cudaErrorInvalidValue;
   IdxArgs a{s,
             plan,
             w_operand,
@@ -1020,10 +1038,14 @@ cudaError_t launch_index_scores(const SeqsDev& s, const PlanBufs& plan, int tg, 
     // the rows' CTAs wait on one another: every CTA must be resident (one per
     // SM) and hold at most the capacity the workspace was sized for
     if (tg != 1 || grid < kFusedGrid) return cudaErrorInvalidConfiguration;
+    if (mx4) return launch_tc<false, 1, true, true, true>(mk, mq, a, kFusedGrid, st);
     if (mx) return launch_tc<false, 1, true, true>(mk, mq, a, kFusedGrid, st);
     return bf16 ? launch_tc<true, 1, true>(mk, mq, a, kFusedGrid, st) : launch_tc<false, 1, true>(mk, mq, a, kFusedGrid, st);
   }
-  if (mx) {
+  if (mx4) {
+    if (tg == 1) return launch_tc<false, 1, false, true, true>(mk, mq, a, grid, st);
+    if (tg == 2) return launch_tc<false, 2, false, true, true>(mk, mq, a, grid, st);
+  } else if (mx) {
     if (tg == 1) return launch_tc<false, 1, false, true>(mk, mq, a, grid, st);
     if (tg == 2) return launch_tc<false, 2, false, true>(mk, mq, a, grid, st);
   } else if (!bf16) {

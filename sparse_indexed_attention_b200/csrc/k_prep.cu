@@ -14,7 +14,7 @@
 //   [T, 64, 4] for the indexer's block-scaled MMA.
 #include <cuda_fp8.h>
 
-#include "dsa_internal.cuh"
+#include "mx4.cuh"
 
 namespace dsa {
 
@@ -384,7 +384,8 @@ struct PrepArgs {
   const float* w;
   uint8_t* codes;
   float* w_scaled;
-  uint8_t* q_sf;  // MXFP8: E8M0 group scales [rows, 4] (w_scaled unused)
+  uint8_t* q_sf;  // MXFP8 / MXFP4: E8M0 group scales [rows, 4] (w_scaled unused)
+  bool mx4;
   int quant_rows;
   uint32_t* zero;
   int64_t zero_words;
@@ -398,7 +399,10 @@ __global__ void __launch_bounds__(1024) k_prep(const PrepArgs a) {
     return;
   }
   const int b = blockIdx.x - 1, nb = gridDim.x - 1;
-  if (a.qI) {
+  if (a.qI && a.mx4) {  // two rows per warp
+    const int64_t row = (int64_t)b * 64 + threadIdx.x / mx4::kPieces;
+    mx4::quantize_row(a.qI, row, a.codes, a.q_sf, row, row < a.quant_rows);
+  } else if (a.qI) {
     const int row = b * 32 + (threadIdx.x >> 5);
     if (row < a.quant_rows) {
       if (a.q_sf)
@@ -415,11 +419,12 @@ __global__ void __launch_bounds__(1024) k_prep(const PrepArgs a) {
 }
 
 cudaError_t launch_prep(const SeqsDev& s, int tg, int ch, const PlanBufs& plan, const __nv_bfloat16* qI,
-                        const float* w, uint8_t* codes, float* w_scaled, uint8_t* q_sf, uint32_t* zero,
+                        const float* w, uint8_t* codes, float* w_scaled, uint8_t* q_sf, bool mx4, uint32_t* zero,
                         int64_t zero_words, uint32_t* err, cudaStream_t st) {
-  PrepArgs a{s,     tg,   ch, plan, err, qI, w, codes, w_scaled, q_sf, qI ? s.num_tokens * kHI : 0,
+  PrepArgs a{s,   tg,   ch, plan, err, qI, w, codes, w_scaled, q_sf, mx4, qI ? s.num_tokens * kHI : 0,
              zero, zero ? zero_words : 0};
-  const int64_t nq = qI ? ((int64_t)s.num_tokens * kHI + 31) / 32 : 0;
+  const int per = mx4 ? 64 : 32;  // query rows per block
+  const int64_t nq = qI ? ((int64_t)s.num_tokens * kHI + per - 1) / per : 0;
   const int64_t nz = zero ? (zero_words + 4095) / 4096 : 0;
   const int64_t extra = nq > nz ? nq : nz;
   cudaError_t e = launch_pdl("prep", k_prep, dim3((unsigned)(1 + extra)), dim3(1024), 0, st, a);

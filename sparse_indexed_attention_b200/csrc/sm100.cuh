@@ -378,6 +378,29 @@ __device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
+// kind::mxf4.block_scale: packed E2M1 operands, K = 64 per instruction and two
+// scale bytes per row of each (scale_vec::2X); sf_id 0 or 2 picks the byte
+// pair of each 32-bit scale column.  Same scale layout and address form as
+// mma_mx.
+__host__ __device__ constexpr uint32_t make_idesc_mx4(int M, int N, int sf_id) {
+  return make_idesc_mx(M, N, sf_id) | (1u << 7)  // A: E2M1
+         | (1u << 10);                           // B: E2M1
+}
+
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// K-major operand of 64-byte rows in the 64-byte swizzle (8-row groups 512
+// bytes apart, atoms 512-byte aligned); K steps advance inside the row as in
+// sw128_kmajor_desc.
+__device__ __forceinline__ uint64_t sw64_kmajor_desc(uint32_t saddr) { return smem_desc(saddr, 16, 512, 4); }
+
 // 32 rows x 128 bits from shared memory into TMEM columns [taddr, taddr + 4),
 // the same 32 rows written to lanes 0-31 of each of the four lane quarters
 // (the scale-factor layout above).  Executes in order with this thread's MMAs.
