@@ -128,7 +128,10 @@ typedef enum {
   DSA_OP_SPARSE_MLA = 3,
   DSA_OP_INDEX_TOPK_ATTN = 4,
   DSA_OP_INDEX_TOPK_ATTN_FUSED = 5, /* dsa_index_topk_attn_ex with DSA_SELECT_IN_INDEXER */
-  DSA_OP_APPEND_INDEX_KEYS = 6
+  DSA_OP_APPEND_INDEX_KEYS = 6,
+  DSA_OP_ATTN_MASS = 7,
+  DSA_OP_EVICT_SELECT = 8,
+  DSA_OP_EVICT_COMPACT = 9  /* num_phys_pages = pages of the destination pools */
 } dsa_op_t;
 
 /* Flags of dsa_index_topk_attn_ex. */
@@ -155,6 +158,19 @@ enum {
   DSA_ROPE_POS64 = 4,     /* positions are int64 (else int32)                        */
   DSA_ROPE_MAX_DIM = 1024 /* the largest rot_dim                                     */
 };
+
+enum {
+  DSA_MASS_FRACTION_BITS = 40, /* attention mass is in units of 2^-40           */
+  DSA_MAX_POOLS = 8            /* pools one dsa_evict_compact call moves        */
+};
+
+/* One pool of a paged cache for dsa_evict_compact: rows of row_bytes bytes,
+ * moved from src to dst (the same array to compact inside the pool). */
+typedef struct {
+  const void *src;
+  void *dst;
+  int32_t row_bytes;           /* a multiple of 4, 4 .. 65536                   */
+} dsa_pool_t;
 
 /* Batch geometry (host struct; the three arrays are device memory).
  *   batch          B >= 1 sequences
@@ -378,6 +394,61 @@ dsa_status_t dsa_index_topk_attn_ex(const dsa_seqs_t *seqs, const void *qI,
                                     int32_t *idx_out, void *ws, size_t ws_bytes,
                                     unsigned flags, dsa_event_t q_ready,
                                     dsa_stream_t stream);
+
+/* Accumulated attention weight, the ranking of cache eviction.  For every query
+ * token t of sequence b and every selected position s in idx[t]:
+ *   mass[b*ld + s] += 2^40 / H * sum_h exp(scale * q[t,h,:] . KV[s,0:576] - lse[t,h])
+ * the weight the token's attention gave s, averaged over heads and limited to
+ * [0, 1] (NaN adds nothing), rounded to an integer.  Integer sums: the result
+ * does not depend on the order of additions.  q, kv, kv_scale, kv_dtype, idx, K,
+ * H and scale are those of dsa_sparse_mla_fwd_ex, lse its lse.  idx entries of -1
+ * add nothing; an entry outside -1..pos(t) is skipped and sets
+ * DSA_ERR_BAD_INDEX.
+ *   mass int64 [B, ld], ld >= max_ctx, 16-byte aligned; other entries untouched.
+ * Workspace: DSA_OP_ATTN_MASS (the error word). */
+dsa_status_t dsa_attn_mass(const dsa_seqs_t *seqs, const void *q, const void *kv,
+                           const void *kv_scale, dsa_kv_dtype_t kv_dtype,
+                           const int32_t *idx, int K, int H, float scale,
+                           const float *lse, int64_t *mass, int64_t ld, void *ws,
+                           size_t ws_bytes, dsa_stream_t stream);
+
+/* Which positions of each sequence stay in a cache cut back to `budget` rows.
+ * A sequence of at most budget positions keeps them all.  A longer one keeps its
+ * first `sink` and last `recent` positions and, of the others, those of the
+ * largest mass; masses are compared after rounding to fp32, ties keep the lower
+ * position.  keep int32 [B, budget]: the kept positions ascending, then -1;
+ * keep_len int32 [B]: how many.  Any budget (not bound to the K of dsa_topk).
+ *   ctx_len int32 [B], 0 <= ctx_len <= max_ctx (else the sequence keeps nothing
+ *   and DSA_ERR_BAD_INDEX is set); mass int64 [B, ld]; recent + sink <= budget;
+ *   max_ctx and budget at most 2^30.
+ * Workspace: DSA_OP_EVICT_SELECT (the error word). */
+dsa_status_t dsa_evict_select(const int32_t *ctx_len, int B, int max_ctx,
+                              const int64_t *mass, int64_t ld, int budget,
+                              int recent, int sink, int32_t *keep,
+                              int32_t *keep_len, void *ws, size_t ws_bytes,
+                              dsa_stream_t stream);
+
+/* Moves the kept rows of every pool of a paged cache to new pages: for i <
+ * keep_len[b], the row of logical position keep[b*budget + i] of sequence b (by
+ * seqs' page table) becomes row i of its new cache (by new_page_table, int32
+ * [B, new_max_pages], page ids below new_num_pages, the pages of each dst).
+ * Afterwards the sequence has ctx_len = keep_len[b] and the new table; rows keep
+ * what was stored in them (rope dims stay at the angles they were written with).
+ * mass / new_mass (both NULL, or int64 [B, ld] and [B, new_ld]) move alike.
+ * Rows past keep_len are left as they were.
+ * A new page must not be used twice, nor (for a pool compacted inside itself) be
+ * one that any sequence of the batch reads: such a page, a bad page id or a keep
+ * entry outside 0..ctx_len-1 is not written and sets DSA_ERR_BAD_INDEX.  A dst
+ * that is not its own src must share no byte with any other array of the call.
+ * seqs->q_seq_start is not read.  new_max_pages * 64 and new_ld >= min(budget,
+ * max_ctx).  Workspace: DSA_OP_EVICT_COMPACT. */
+dsa_status_t dsa_evict_compact(const dsa_seqs_t *seqs, const int32_t *keep,
+                               const int32_t *keep_len, int budget,
+                               const int32_t *new_page_table, int new_max_pages,
+                               int new_num_pages, const dsa_pool_t *pools,
+                               int num_pools, const int64_t *mass, int64_t ld,
+                               int64_t *new_mass, int64_t new_ld, void *ws,
+                               size_t ws_bytes, dsa_stream_t stream);
 
 /* Rotary positions, the input preparation of the queries and keys ([P2]
  * section 4(2) prepares them ahead of the indexer and the attention: the rope

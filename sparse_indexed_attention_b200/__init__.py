@@ -37,8 +37,10 @@ DSA_KV_BF16, DSA_KV_FP8_E4M3 = 0, 1
 DSA_OUT_BF16, DSA_OUT_F32 = 0, 1
 DSA_NOALLOC_SCRATCH_BYTES = 32 << 20
 DSA_OP_QUANTIZE_INDEX_QUERY, DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_INDEX_TOPK_ATTN, \
-    DSA_OP_INDEX_TOPK_ATTN_FUSED, DSA_OP_APPEND_INDEX_KEYS = range(7)
+    DSA_OP_INDEX_TOPK_ATTN_FUSED, DSA_OP_APPEND_INDEX_KEYS, DSA_OP_ATTN_MASS, DSA_OP_EVICT_SELECT, \
+    DSA_OP_EVICT_COMPACT = range(10)
 DSA_SELECT_IN_INDEXER = 1
+DSA_MASS_FRACTION_BITS, DSA_MAX_POOLS = 40, 8
 DSA_ROPE_BF16, DSA_ROPE_F16, DSA_ROPE_F32 = range(3)
 DSA_ROPE_HALF, DSA_ROPE_TRANSPOSE, DSA_ROPE_POS64, DSA_ROPE_MAX_DIM = 1, 2, 4, 1024
 
@@ -49,6 +51,7 @@ EXPORTS = ("dsa_workspace_size",
            "dsa_index_scores", "dsa_topk",
            "dsa_sparse_mla_fwd", "dsa_sparse_mla_fwd_ex", "dsa_sparse_mla_fwd_noalloc",
            "dsa_index_topk_attn", "dsa_index_topk_attn_ex",
+           "dsa_attn_mass", "dsa_evict_select", "dsa_evict_compact",
            "dsa_rope",
            "dsa_check_error", "dsa_check_error_noalloc", "dsa_set_wait_limit_ns",
            "dsa_launches_in_last_call", "dsa_launch_timing", "dsa_last_launch_times", "dsa_status_string")
@@ -58,6 +61,10 @@ class DsaSeqsC(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_q_tokens", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("num_phys_pages", ctypes.c_int32), ("max_ctx", ctypes.c_int32),
                 ("q_seq_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class DsaPoolC(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -83,6 +90,12 @@ _sig = {
     "dsa_index_topk_attn_ex": (ctypes.c_int, [_SEQ, _P, _P, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int,
                                               ctypes.c_int, ctypes.c_int, _F, _P, ctypes.c_int, _P, _P, _P, _SZ,
                                               ctypes.c_uint, _P, _P]),
+    "dsa_attn_mass": (ctypes.c_int, [_SEQ, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, _F, _P, _P, _I64,
+                                     _P, _SZ, _P]),
+    "dsa_evict_select": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, _P, _I64, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, _P, _P, _P, _SZ, _P]),
+    "dsa_evict_compact": (ctypes.c_int, [_SEQ, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int,
+                                         ctypes.POINTER(DsaPoolC), ctypes.c_int, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "dsa_rope": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64, _I64, _I64, _I64,
                                 _P, _P, ctypes.c_int, ctypes.c_int, _F, ctypes.c_uint, _P]),
     "dsa_check_error": (ctypes.c_int, [_P, _P]),
@@ -297,7 +310,11 @@ def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     Every call that is not given `ws` uses this cached buffer, whatever its
     stream.  Calls that may run at the same time on different streams must
     each pass a workspace of their own: the library requires that concurrent
-    calls do not share one (its first word is the sticky error flag)."""
+    calls do not share one (its first word is the sticky error flag).
+
+    During stream capture a buffer that is not cached yet belongs to the graph
+    alone (its zeroing is part of the graph and has not run), so it is not
+    cached; a captured call whose error flag is to be read passes its own."""
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
@@ -305,6 +322,8 @@ def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     ws = _ws_cache.get(k)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            return ws
         _ws_cache[k] = ws
     return ws
 
@@ -514,6 +533,114 @@ def dsa_index_topk_attn(seqs: Seqs, qI, w, kI, kI_scale, q, kv, K: int, scale: f
                                        DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev, _stream(q.device)),
            "dsa_index_topk_attn")
     return out, lse
+
+
+_I64T = (torch.int64,)
+
+
+def dsa_attn_mass(seqs: Seqs, q, kv, idx, lse, scale: float, mass, kv_scale=None, ws=None):
+    """Adds to mass [B, at least max_ctx] int64 the attention weight that this
+    call's tokens give each selected position, averaged over heads, in units of
+    2^-DSA_MASS_FRACTION_BITS: q, kv, idx, scale, kv_scale as dsa_sparse_mla_fwd
+    took them, lse [T, H] as it returned it.  Returns mass."""
+    dev = _cuda_device(q, "q")
+    _need_seqs(seqs, dev)
+    T, rows = seqs.num_q_tokens, seqs.num_phys_pages * 64
+    _need(q, "q", _BF16T, (T, None, 576), dev)
+    H = q.shape[1]
+    if kv_scale is None:
+        _need(kv, "kv", _BF16T, (None, 576), dev, rows)
+    else:
+        _need(kv, "kv", _FP8T, (None, 576), dev, rows)
+        _need(kv_scale, "kv_scale", _U8T, (None, 8), dev, rows)
+    _need(idx, "idx", _I32T, (T, None), dev)
+    _need(lse, "lse", _F32T, (T, H), dev)
+    _need(mass, "mass", _I64T, (seqs.batch, None), dev)
+    if mass.shape[1] < seqs.max_ctx:
+        raise ValueError(f"mass: {mass.shape[1]} positions per sequence, max_ctx is {seqs.max_ctx}")
+    c = seqs.c()
+    ws = ws if ws is not None else workspace(256, dev, "attn_mass")
+    _need_ws(ws, dev)
+    with _on(dev):
+        _check(_lib.dsa_attn_mass(ctypes.byref(c), q.data_ptr(), kv.data_ptr(), _ptr(kv_scale),
+                                  DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3, idx.data_ptr(), idx.shape[1],
+                                  H, scale, lse.data_ptr(), mass.data_ptr(), mass.shape[1], ws.data_ptr(), ws.numel(),
+                                  _stream(dev)), "dsa_attn_mass")
+    return mass
+
+
+def dsa_evict_select(ctx_len, mass, budget: int, recent: int = 0, sink: int = 0, keep=None, keep_len=None, ws=None):
+    """(keep [B, budget] int32, keep_len [B] int32): the positions each
+    sequence keeps when its cache is cut back to `budget` rows -- all if it has
+    no more, else the first `sink`, the last `recent` and those of the largest
+    mass [B, *] int64 -- ascending, -1 behind them."""
+    dev = _cuda_device(mass, "mass")
+    _need(mass, "mass", _I64T, (None, None), dev)
+    B, ld = mass.shape
+    _need(ctx_len, "ctx_len", _I32T, (B,), dev)
+    if budget < 1 or recent < 0 or sink < 0 or recent + sink > budget:
+        raise ValueError(f"budget={budget}, recent={recent}, sink={sink}: expected recent + sink <= budget, budget >= 1")
+    keep = keep if keep is not None else torch.empty((B, budget), dtype=torch.int32, device=dev)
+    keep_len = keep_len if keep_len is not None else torch.empty((B,), dtype=torch.int32, device=dev)
+    _need(keep, "keep", _I32T, (B, budget), dev)
+    _need(keep_len, "keep_len", _I32T, (B,), dev)
+    ws = ws if ws is not None else workspace(256, dev, "evict_select")
+    _need_ws(ws, dev)
+    with _on(dev):
+        _check(_lib.dsa_evict_select(ctx_len.data_ptr(), B, ld, mass.data_ptr(), ld, budget, recent, sink,
+                                     keep.data_ptr(), keep_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
+               "dsa_evict_select")
+    return keep, keep_len
+
+
+def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=None, new_mass=None, ws=None):
+    """Moves the kept rows of each pool to the new pages.  `pools`: up to
+    DSA_MAX_POOLS pools [R, ...], each compacted inside itself (its new pages
+    must not be pages that seqs reads), or pairs (pool, destination pool).
+    mass, new_mass int64 [B, *] move alike.  Afterwards the batch is
+    Seqs(..., ctx_len=keep_len, page_table=new_page_table, ...)."""
+    dev = _cuda_device(keep, "keep")
+    _need_seqs(seqs, dev)
+    B = seqs.batch
+    _need(keep, "keep", _I32T, (B, None), dev)
+    _need(keep_len, "keep_len", _I32T, (B,), dev)
+    _need(new_page_table, "new_page_table", _I32T, (B, None), dev)
+    n = len(pools)
+    if n > DSA_MAX_POOLS:
+        raise ValueError(f"{n} pools, at most {DSA_MAX_POOLS}")
+    cp = (DsaPoolC * max(n, 1))()
+    pages = seqs.num_phys_pages
+    new_pages = None
+    for i, p in enumerate(pools):
+        src, dst = p if isinstance(p, (tuple, list)) else (p, p)
+        for t, name in ((src, f"pools[{i}]"), (dst, f"pools[{i}] destination")):
+            if not isinstance(t, torch.Tensor) or t.dim() < 1:
+                raise TypeError(f"{name}: expected a tensor of rows")
+            _need(t, name, (src.dtype,), (None, *src.shape[1:]), dev)
+        if src.shape[0] < pages * 64:
+            raise ValueError(f"pools[{i}]: {src.shape[0]} rows, the page pool needs at least {pages * 64}")
+        if dst.shape[0] < 64:
+            raise ValueError(f"pools[{i}] destination: less than a page of rows")
+        here = pages if dst is src else dst.shape[0] // 64
+        new_pages = here if new_pages is None else min(new_pages, here)
+        cp[i].src, cp[i].dst = src.data_ptr(), dst.data_ptr()
+        cp[i].row_bytes = src.numel() // src.shape[0] * src.element_size()
+    new_pages = pages if new_pages is None else new_pages
+    ld = new_ld = 0
+    if mass is not None or new_mass is not None:
+        _need(mass, "mass", _I64T, (B, None), dev)
+        _need(new_mass, "new_mass", _I64T, (B, None), dev)
+        ld, new_ld = mass.shape[1], new_mass.shape[1]
+    c = seqs.c()
+    need = 256 + (3 * ((new_pages + 31) // 32) * 4 + 255) // 256 * 256
+    # one cached buffer per size: a captured call's buffer is never replaced by a larger one
+    ws = ws if ws is not None else workspace(need, dev, ("evict_compact", need))
+    _need_ws(ws, dev)
+    with _on(dev):
+        _check(_lib.dsa_evict_compact(ctypes.byref(c), keep.data_ptr(), keep_len.data_ptr(), keep.shape[1],
+                                      new_page_table.data_ptr(), new_page_table.shape[1], new_pages, cp, n, _ptr(mass),
+                                      ld, _ptr(new_mass), new_ld, ws.data_ptr(), ws.numel(), _stream(dev)),
+               "dsa_evict_compact")
 
 
 _ROPE_DTYPES = {torch.bfloat16: DSA_ROPE_BF16, torch.float16: DSA_ROPE_F16, torch.float32: DSA_ROPE_F32}

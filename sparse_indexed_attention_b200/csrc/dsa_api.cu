@@ -24,7 +24,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // the sticky error word.
 struct Layout {
   size_t tok_seq = 0, tok_pos = 0, seq_gstart = 0, groups = 0, items = 0, counts = 0;
-  size_t q_codes = 0, w_scaled = 0, q_sf = 0, scores = 0, idx = 0, topk = 0, partials = 0, tail = 0, cand = 0;
+  size_t q_codes = 0, w_scaled = 0, q_sf = 0, scores = 0, idx = 0, topk = 0, partials = 0, tail = 0, cand = 0, bitmaps = 0;
   size_t total = 0;
   int64_t ld = 0;
   bool fused = false;       // the indexer selects the Top-K itself (no score scratch)
@@ -35,7 +35,7 @@ struct Layout {
 // it is sized for the smaller group (more groups, more items).
 int sizing_group_tokens(int T, int B) { return T == B ? 1 : 2; }
 
-Layout make_layout(dsa_op_t op, int T, int B, int max_ctx, int K, int H) {
+Layout make_layout(dsa_op_t op, int T, int B, int max_ctx, int K, int H, int pages = 0) {
   Layout L;
   size_t off = kAlign;  // header: the sticky error word
   auto take = [&](size_t bytes) {
@@ -75,6 +75,7 @@ Layout make_layout(dsa_op_t op, int T, int B, int max_ctx, int K, int H) {
       L.topk = take(topk_scratch_bytes(T, L.ld, K));
     }
   }
+  if (op == DSA_OP_EVICT_COMPACT) L.bitmaps = take(evict_bitmap_bytes(pages));
   if (op == DSA_OP_TOPK) L.topk = take(topk_scratch_bytes(T, max_ctx, K));
   if (op == DSA_OP_SPARSE_MLA || op == DSA_OP_INDEX_TOPK_ATTN) L.partials = take(sparse_mla_partials_bytes(T, K, H));
   L.total = off;
@@ -212,8 +213,10 @@ size_t dsa_workspace_size(dsa_op_t op, const dsa_seqs_t* seqs, int K, int H) {
   if (!seqs || seqs->num_q_tokens < 1 || seqs->max_ctx < 1) return 0;
   if (op == DSA_OP_QUANTIZE_INDEX_QUERY) return 0;
   if (op == DSA_OP_TOPK) return make_layout(op, seqs->num_q_tokens, 1, seqs->max_ctx, K, 16).total;
-  if (op < 0 || op > DSA_OP_APPEND_INDEX_KEYS) return 0;
+  if (op < 0 || op > DSA_OP_EVICT_COMPACT) return 0;
   if (seqs->batch < 1) return 0;
+  if (op == DSA_OP_EVICT_COMPACT)
+    return seqs->num_phys_pages < 1 ? 0 : make_layout(op, 1, 1, 1, 1, 16, seqs->num_phys_pages).total;
   if ((op == DSA_OP_SPARSE_MLA || op == DSA_OP_INDEX_TOPK_ATTN || op == DSA_OP_INDEX_TOPK_ATTN_FUSED) &&
       (K < 1 || K > kMaxK || !valid_H(H)))
     return 0;
@@ -397,6 +400,79 @@ dsa_status_t dsa_index_topk_attn(const dsa_seqs_t* seqs, const void* qI, const f
                                  int32_t* idx_out, void* ws, size_t ws_bytes, dsa_stream_t stream) {
   return dsa_index_topk_attn_ex(seqs, qI, w, kI, kI_scale, ki_dtype, q, kv, nullptr, DSA_KV_BF16, K, H, scale, out,
                                 out_dtype, lse, idx_out, ws, ws_bytes, 0u, nullptr, stream);
+}
+
+dsa_status_t dsa_attn_mass(const dsa_seqs_t* seqs, const void* q, const void* kv, const void* kv_scale,
+                           dsa_kv_dtype_t kv_dtype, const int32_t* idx, int K, int H, float scale, const float* lse,
+                           int64_t* mass, int64_t ld, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  g_launches = 0;
+  DSA_TRY(check_attn_args(seqs, q, kv, K, H, scale, mass, DSA_OUT_F32, lse));
+  DSA_TRY(check_kv_args(kv_scale, kv_dtype));
+  if (!idx || !lse || !aligned(idx, 4) || ld < seqs->max_ctx) return DSA_ERR_INVALID_ARG;
+  DSA_TRY(check_ws(ws, ws_bytes, kAlign));
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_attn_mass(to_dev(seqs), reinterpret_cast<const __nv_bfloat16*>(q), kv,
+                                      static_cast<const uint8_t*>(kv_scale), idx, K, H, scale, lse, mass, ld,
+                                      at<uint32_t>(ws, 0), (cudaStream_t)stream));
+}
+
+dsa_status_t dsa_evict_select(const int32_t* ctx_len, int B, int max_ctx, const int64_t* mass, int64_t ld, int budget,
+                              int recent, int sink, int32_t* keep, int32_t* keep_len, void* ws, size_t ws_bytes,
+                              dsa_stream_t stream) {
+  g_launches = 0;
+  if (!ctx_len || !mass || !keep || !keep_len || B < 1 || max_ctx < 1 || ld < max_ctx) return DSA_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || sink < 0 || recent > budget || sink > budget - recent) return DSA_ERR_INVALID_ARG;
+  if (!aligned(ctx_len, 4) || !aligned(mass, 8) || !aligned(keep, 4) || !aligned(keep_len, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (B > INT32_MAX / 8 || max_ctx > (1 << 30) || budget > (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  DSA_TRY(check_ws(ws, ws_bytes, kAlign));
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_evict_select(ctx_len, B, max_ctx, mass, ld, budget, recent, sink, keep, keep_len,
+                                         at<uint32_t>(ws, 0), (cudaStream_t)stream));
+}
+
+dsa_status_t dsa_evict_compact(const dsa_seqs_t* seqs, const int32_t* keep, const int32_t* keep_len, int budget,
+                               const int32_t* new_page_table, int new_max_pages, int new_num_pages,
+                               const dsa_pool_t* pools, int num_pools, const int64_t* mass, int64_t ld,
+                               int64_t* new_mass, int64_t new_ld, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  g_launches = 0;
+  DSA_TRY(check_seqs(seqs));
+  if (!keep || !keep_len || !new_page_table || budget < 1 || new_max_pages < 1 || new_num_pages < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (budget > (1 << 30) || (int64_t)new_num_pages * kPage > (int64_t)INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (!aligned(keep, 4) || !aligned(keep_len, 4) || !aligned(new_page_table, 4)) return DSA_ERR_INVALID_ARG;
+  const int most = budget < seqs->max_ctx ? budget : seqs->max_ctx;  // rows a sequence can keep
+  if ((int64_t)new_max_pages * kPage < most) return DSA_ERR_INVALID_ARG;
+  if (num_pools < 0 || num_pools > DSA_MAX_POOLS || (num_pools > 0 && !pools)) return DSA_ERR_INVALID_ARG;
+  auto disjoint = [](const void* p, int64_t np, const void* q, int64_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a + (uint64_t)np <= b || b + (uint64_t)nq <= a;
+  };
+  auto src_bytes = [&](int i) { return (int64_t)seqs->num_phys_pages * kPage * pools[i].row_bytes; };
+  auto dst_bytes = [&](int i) { return (int64_t)new_num_pages * kPage * pools[i].row_bytes; };
+  for (int i = 0; i < num_pools; ++i) {
+    const dsa_pool_t& p = pools[i];
+    if (!p.src || !p.dst || !aligned(p.src, 16) || !aligned(p.dst, 16)) return DSA_ERR_INVALID_ARG;
+    if (p.row_bytes < 4 || p.row_bytes % 4 || p.row_bytes > 65536) return DSA_ERR_UNSUPPORTED;
+    // a destination is its own source's array, or shares no byte with any array of the call
+    for (int j = 0; j < num_pools; ++j) {
+      if (!disjoint(p.dst, dst_bytes(i), pools[j].src, src_bytes(j)) && !(i == j && p.src == p.dst))
+        return DSA_ERR_INVALID_ARG;
+      if (i != j && !disjoint(p.dst, dst_bytes(i), pools[j].dst, dst_bytes(j))) return DSA_ERR_INVALID_ARG;
+    }
+  }
+  if ((mass == nullptr) != (new_mass == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (mass) {
+    if (!aligned(mass, 8) || !aligned(new_mass, 8) || ld < seqs->max_ctx || new_ld < most) return DSA_ERR_INVALID_ARG;
+    if (!disjoint(mass, seqs->batch * ld * 8, new_mass, seqs->batch * new_ld * 8)) return DSA_ERR_INVALID_ARG;
+  }
+  const Layout L = make_layout(DSA_OP_EVICT_COMPACT, 1, 1, 1, 1, 16, new_num_pages);
+  DSA_TRY(check_ws(ws, ws_bytes, L.total));
+  timer_begin((cudaStream_t)stream);
+  return cuda_status(launch_evict_compact(to_dev(seqs),
+                                          EvictMove{keep, keep_len, budget, new_page_table, new_max_pages,
+                                                    new_num_pages, pools, num_pools, mass, new_mass, ld, new_ld},
+                                          at<void>(ws, L.bitmaps), at<uint32_t>(ws, 0), (cudaStream_t)stream));
 }
 
 dsa_status_t dsa_rope(const void* x, void* out, int dtype, int T, int H, int D, int64_t x_stride_t, int64_t x_stride_h,

@@ -256,6 +256,28 @@ cudaError_t launch_append_index_keys_mx4(const SeqsDev& s, const __nv_bfloat16* 
 cudaError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, __nv_bfloat16* out,
                                   cudaStream_t st);
 
+// Eviction (k_attn_mass.cu, k_evict.cu).
+cudaError_t launch_attn_mass(const SeqsDev& s, const __nv_bfloat16* q, const void* kv, const uint8_t* kv8_scale,
+                             const int32_t* idx, int K, int H, float scale, const float* lse, int64_t* mass,
+                             int64_t ld, uint32_t* err, cudaStream_t st);
+cudaError_t launch_evict_select(const int32_t* ctx_len, int B, int max_ctx, const int64_t* mass, int64_t ld, int budget,
+                                int recent, int sink, int32_t* keep, int32_t* keep_len, uint32_t* err,
+                                cudaStream_t st);
+struct EvictMove {
+  const int32_t* keep;
+  const int32_t* keep_len;
+  int budget;
+  const int32_t* new_table;
+  int new_max_pages, new_pages;
+  const dsa_pool_t* pools;
+  int npools;
+  const int64_t* mass;
+  int64_t* new_mass;
+  int64_t ld, new_ld;
+};
+size_t evict_bitmap_bytes(int pages);
+cudaError_t launch_evict_compact(const SeqsDev& s, const EvictMove& m, void* bitmaps, uint32_t* err, cudaStream_t st);
+
 // Rotary positions (arguments checked by dsa_rope; strides in elements).
 struct RopeCall {
   const void* x;

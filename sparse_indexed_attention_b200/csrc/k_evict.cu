@@ -1,0 +1,359 @@
+// Eviction from the paged caches by accumulated attention weight: which
+// positions of each sequence stay (select), and their rows, moved to new pages
+// (mark + compact).
+//
+// select.  The budget's largest of a row of keys, ties to the lower position.  A
+// key is the mass rounded to fp32, order-preserving in 32 bits (24 bits of a
+// ranking statistic; 64-bit keys would double the digits of the radix select);
+// the positions that always stay -- the first `sink`, the last `recent` --
+// have the largest key.  One cluster of CTAs takes a sequence, each a run of
+// its positions with the keys in shared memory, read from HBM once.  The
+// cluster resolves the budget's key digit by digit (11, 11, 10 bits): every
+// CTA counts its keys, and each sums all the CTAs' histograms through
+// distributed shared memory and finds the same bin.  Counts before each CTA give
+// the output offsets, so the positions come out ascending.  Latency bound: four
+// cluster barriers and a scan.  MEASURED-SELECT
+//
+// mark.  A destination page must be no page that the call reads and no
+// destination twice, or rows would be overwritten while others still read
+// them.  One cluster checks this on bitmaps over the pool's pages, so that a bad
+// table is an error and not a race.
+//
+// compact.  A block takes one destination page of one sequence: 64 rows of
+// every pool, 16 bytes per access where the row size allows.  HBM bound: each
+// kept byte is read once and written once.  MEASURED-COMPACT
+#include <cooperative_groups.h>
+
+#include "topk_select.cuh"
+
+namespace dsa {
+
+namespace {
+
+namespace cg = cooperative_groups;
+using topk::kD1Bins;
+using topk::kD2Bins;
+using topk::kD3Bins;
+
+constexpr int kSelThreads = 1024;
+constexpr int kCluster = 8;                    // CTAs per sequence (the portable cluster size)
+constexpr int kSlotsMax = 40960;               // keys a CTA keeps in shared memory (160 KB)
+constexpr uint32_t kForced = 0xFFFFFFFFu;      // above any key of a number
+
+struct SelectArgs {
+  const int32_t* ctx_len;
+  const int64_t* mass;
+  int64_t ld;
+  int max_ctx, budget, recent, sink;
+  int32_t* keep;
+  int32_t* keep_len;
+  uint32_t* err;
+};
+
+struct SelectSmem {
+  uint32_t hist[kD1Bins + kD2Bins + kD3Bins];  // this CTA's counts, one table per digit
+  uint32_t sum[kD1Bins];                       // the cluster's counts of the current digit
+  uint32_t buf[33];
+  uint32_t bin, above, gt, eq;
+};
+
+// kStaged: the CTA's keys fit in shared memory; otherwise each pass reads the
+// masses again (from L2 in the main).
+template <bool kStaged>
+__global__ void __launch_bounds__(kSelThreads) k_evict_select(const SelectArgs a) {
+  extern __shared__ uint32_t keys[];
+  __shared__ SelectSmem sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = blockIdx.x / C, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int n = __ldg(a.ctx_len + b);
+  int32_t* keep = a.keep + (int64_t)b * a.budget;
+  const bool bad = n < 0 || n > a.max_ctx;
+  const int kept = bad ? 0 : min(n, a.budget);
+  for (int i = kept + rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads) keep[i] = -1;
+  if (rank == 0 && tid == 0) {
+    a.keep_len[b] = kept;
+    if (bad) raise_error(a.err, kErrBadIndex);
+  }
+  if (kept == n || bad) {  // nothing to choose; the same for the whole cluster
+    for (int i = rank * kSelThreads + tid; i < kept; i += C * kSelThreads) keep[i] = i;
+    return;
+  }
+  const int per = ((n + C - 1) / C + 3) & ~3;
+  const int s0 = min(n, rank * per), len = min(n, s0 + per) - s0;
+  const int64_t* mass = a.mass + (int64_t)b * a.ld + s0;
+  auto key_of = [&](int i) -> uint32_t {
+    const int s = s0 + i;
+    return s < a.sink || s >= n - a.recent ? kForced : order_key(__ll2float_rn(__ldg(mass + i)));
+  };
+  auto key_at = [&](int i) -> uint32_t { return kStaged ? keys[i] : key_of(i); };
+  for (int i = tid; i < kD1Bins + kD2Bins + kD3Bins; i += kSelThreads) sm.hist[i] = 0u;
+  __syncthreads();
+  uint32_t prefix = 0, need = (uint32_t)a.budget;
+  for (int level = 0; level < 3; ++level) {
+    const int off = level == 0 ? 0 : (level == 1 ? kD1Bins : kD1Bins + kD2Bins), bins = level < 2 ? kD1Bins : kD3Bins;
+    uint32_t* hist = sm.hist + off;
+    for (int i0 = 0; i0 < len; i0 += kSelThreads) {
+      const int i = i0 + tid;
+      bool in = i < len;
+      uint32_t key = 0;
+      if (in) {
+        if (kStaged && level == 0) keys[i] = key = key_of(i);
+        else key = key_at(i);
+      }
+      uint32_t digit;
+      if (level == 0) {
+        digit = topk::digit1(key);
+      } else if (level == 1) {
+        in = in && topk::digit1(key) == prefix;
+        digit = topk::digit2(key);
+      } else {
+        in = in && (key >> 10) == prefix;
+        digit = topk::digit3(key);
+      }
+      hist_add(hist, digit, in);  // never-attended positions share one bin
+    }
+    cluster.sync();
+    for (int d = tid; d < bins; d += kSelThreads) {
+      uint32_t v = 0;
+      for (int r = 0; r < C; ++r) v += cluster.map_shared_rank(hist, r)[d];
+      sm.sum[d] = v;
+    }
+    __syncthreads();
+    if (level < 2)
+      topk::find_bin<kD1Bins>(sm.sum, need, &sm.bin, &sm.above);
+    else
+      topk::find_bin<kD3Bins>(sm.sum, need, &sm.bin, &sm.above);
+    prefix = (prefix << (level < 2 ? 11 : 10)) | sm.bin;
+    need -= sm.above;
+    __syncthreads();
+  }
+  // tau: the budget's key; `need` positions that hold exactly tau stay, the lowest
+  const uint32_t tau = prefix;
+  uint32_t gt = 0, eq = 0;
+  for (int i = tid; i < len; i += kSelThreads) {
+    const uint32_t key = key_at(i);
+    gt += key > tau ? 1u : 0u;
+    eq += key == tau ? 1u : 0u;
+  }
+  uint32_t total;
+  topk::block_scan(gt, sm.buf, &total);
+  if (tid == 0) sm.gt = total;
+  topk::block_scan(eq, sm.buf, &total);
+  if (tid == 0) sm.eq = total;
+  cluster.sync();
+  uint32_t gt_before = 0, eq_before = 0;
+  for (int r = 0; r < rank; ++r) {
+    gt_before += *cluster.map_shared_rank(&sm.gt, r);
+    eq_before += *cluster.map_shared_rank(&sm.eq, r);
+  }
+  const uint32_t taken = min(eq_before, need), at = gt_before + taken;
+  topk::emit_selected(
+      len, tau, need - taken, a.budget - (int)at, [&](int i) { return make_int2(s0 + i, (int)key_at(i)); }, keep + at,
+      sm.buf);
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------- compaction
+
+constexpr int kMoveThreads = 256;
+
+struct MoveArgs {
+  SeqsDev s;
+  const int32_t* keep;
+  const int32_t* keep_len;
+  int budget;
+  const int32_t* new_table;
+  int new_max_pages, new_pages;
+  int npools;
+  const uint8_t* src[DSA_MAX_POOLS];
+  uint8_t* dst[DSA_MAX_POOLS];
+  int row_bytes[DSA_MAX_POOLS], vec[DSA_MAX_POOLS];
+  const int64_t* mass;
+  int64_t* new_mass;
+  int64_t ld, new_ld;
+  bool in_place;           // some pool is its own destination: its pages must not be read
+  uint32_t *read, *written, *twice;  // bitmaps over pages
+  int words;               // of each bitmap
+  uint32_t* err;
+};
+
+// Rows of sequence b that move: none when its lengths are impossible.
+__device__ __forceinline__ int rows_to_move(const MoveArgs& a, int b) {
+  const int n = __ldg(a.keep_len + b), ctx = __ldg(a.s.ctx_len + b);
+  const bool ok = n >= 0 && n <= a.budget && n <= ctx && ctx <= a.s.max_ctx && (ctx + kPage - 1) / kPage <= a.s.max_pages;
+  return ok ? n : -1;
+}
+
+__global__ void __launch_bounds__(1024) k_evict_mark(const MoveArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = (int)cluster.block_rank() * 1024 + threadIdx.x, step = (int)cluster.num_blocks() * 1024;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = tid; i < 3 * a.words; i += step) a.read[i] = 0u;  // the three bitmaps are one run
+  __threadfence();
+  cluster.sync();
+  const int64_t from = a.in_place ? (int64_t)a.s.batch * a.s.max_pages : 0;
+  const int64_t all = from + (int64_t)a.s.batch * a.new_max_pages;
+  for (int64_t i = tid; i < all; i += step) {
+    if (i < from) {
+      const int b = (int)(i / a.s.max_pages), p = (int)(i % a.s.max_pages);
+      const int ctx = __ldg(a.s.ctx_len + b);
+      if (ctx <= a.s.max_ctx && p * kPage < ctx) {
+        const int page = __ldg(a.s.page_table + i);
+        if (page >= 0 && page < a.new_pages) atomicOr(a.read + (page >> 5), 1u << (page & 31));
+      }
+    } else {
+      const int64_t j = i - from;
+      const int b = (int)(j / a.new_max_pages), p = (int)(j % a.new_max_pages);
+      if (p * kPage < rows_to_move(a, b)) {
+        const int page = __ldg(a.new_table + j);
+        if (page >= 0 && page < a.new_pages && (atomicOr(a.written + (page >> 5), 1u << (page & 31)) >> (page & 31) & 1u))
+          atomicOr(a.twice + (page >> 5), 1u << (page & 31));
+      }
+    }
+  }
+}
+
+template <class V>
+__device__ __forceinline__ void move_rows(const uint8_t* src, uint8_t* dst, int row_bytes, const int* rows, int n) {
+  const int nv = row_bytes / (int)sizeof(V), total = n * nv;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < total; i += kMoveThreads) {
+    const int r = i / nv, c = i - r * nv;
+    const int row = rows[r];
+    if (row >= 0)
+      reinterpret_cast<V*>(dst + (int64_t)r * row_bytes)[c] =
+          __ldg(reinterpret_cast<const V*>(src + (int64_t)row * row_bytes) + c);
+  }
+}
+
+// One block: rows 64 p .. 64 p + 63 of sequence b's new cache.
+__global__ void __launch_bounds__(kMoveThreads) k_evict_compact(const MoveArgs a) {
+  __shared__ int rows[kPage];
+  __shared__ int page;
+  const int chunks = (a.budget + kPage - 1) / kPage, b = blockIdx.x / chunks, p = blockIdx.x % chunks, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int kept = rows_to_move(a, b);
+  if (kept < 0 && p == 0 && tid == 0) raise_error(a.err, kErrBadIndex);
+  const int n = min(kPage, kept - p * kPage);
+  if (n <= 0) return;
+  if (tid == 0) {
+    const int d = p < a.new_max_pages ? __ldg(a.new_table + (int64_t)b * a.new_max_pages + p) : -1;
+    bool ok = d >= 0 && d < a.new_pages;
+    if (ok) {
+      const uint32_t bit = 1u << (d & 31);
+      ok = !((a.read[d >> 5] | a.twice[d >> 5]) & bit);
+    }
+    if (!ok) raise_error(a.err, kErrBadIndex);
+    page = ok ? d : -1;
+  }
+  int s = -1, row = -1;
+  if (tid < n) {
+    s = __ldg(a.keep + (int64_t)b * a.budget + p * kPage + tid);
+    if (s >= 0 && s < __ldg(a.s.ctx_len + b))
+      row = (int)phys_row(a.s.page_table, a.s.max_pages, a.s.num_phys_pages, b, s, a.err);
+    else
+      raise_error(a.err, kErrBadIndex);
+    rows[tid] = row;
+  }
+  __syncthreads();
+  if (page < 0) return;
+  if (a.mass && row >= 0)
+    a.new_mass[(int64_t)b * a.new_ld + p * kPage + tid] = __ldg(a.mass + (int64_t)b * a.ld + s);
+  for (int k = 0; k < a.npools; ++k) {
+    uint8_t* dst = a.dst[k] + (int64_t)page * kPage * a.row_bytes[k];
+    if (a.vec[k] == 16)
+      move_rows<uint4>(a.src[k], dst, a.row_bytes[k], rows, n);
+    else if (a.vec[k] == 8)
+      move_rows<uint2>(a.src[k], dst, a.row_bytes[k], rows, n);
+    else
+      move_rows<uint32_t>(a.src[k], dst, a.row_bytes[k], rows, n);
+  }
+}
+
+template <class... KArgs, class... Args>
+cudaError_t launch_cluster(const char* name, void (*kernel)(KArgs...), int grid, int cluster, int threads, size_t smem,
+                           cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e == cudaSuccess) timer_mark(name, st);
+  return e == cudaSuccess ? counted(cudaGetLastError()) : e;
+}
+
+}  // namespace
+
+cudaError_t launch_evict_select(const int32_t* ctx_len, int B, int max_ctx, const int64_t* mass, int64_t ld, int budget,
+                                int recent, int sink, int32_t* keep, int32_t* keep_len, uint32_t* err,
+                                cudaStream_t st) {
+  const SelectArgs a{ctx_len, mass, ld, max_ctx, budget, recent, sink, keep, keep_len, err};
+  // a short row is one CTA's work: its cluster barriers would only add latency
+  const int C = max_ctx <= 4 * kSelThreads ? 1 : kCluster;
+  const int64_t slots = (((int64_t)max_ctx + C - 1) / C + 3) & ~3;
+  if (slots > kSlotsMax) return launch_cluster("evict_select", k_evict_select<false>, B * C, C, kSelThreads, 0, st, a);
+  static thread_local int attr_dev = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (attr_dev != dev) {
+    cudaError_t e =
+        cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotsMax * 4);
+    if (e != cudaSuccess) return e;
+    attr_dev = dev;
+  }
+  return launch_cluster("evict_select", k_evict_select<true>, B * C, C, kSelThreads, (size_t)slots * 4, st, a);
+}
+
+size_t evict_bitmap_bytes(int pages) { return (size_t)3 * (((size_t)pages + 31) / 32) * 4; }
+
+cudaError_t launch_evict_compact(const SeqsDev& s, const EvictMove& m, void* bitmaps, uint32_t* err, cudaStream_t st) {
+  MoveArgs a{};
+  a.s = s;
+  a.keep = m.keep;
+  a.keep_len = m.keep_len;
+  a.budget = m.budget;
+  a.new_table = m.new_table;
+  a.new_max_pages = m.new_max_pages;
+  a.new_pages = m.new_pages;
+  a.npools = m.npools;
+  for (int k = 0; k < m.npools; ++k) {
+    const dsa_pool_t& p = m.pools[k];
+    a.src[k] = static_cast<const uint8_t*>(p.src);
+    a.dst[k] = static_cast<uint8_t*>(p.dst);
+    a.row_bytes[k] = p.row_bytes;
+    a.vec[k] = p.row_bytes % 16 == 0 ? 16 : (p.row_bytes % 8 == 0 ? 8 : 4);
+    a.in_place = a.in_place || p.src == p.dst;
+  }
+  a.mass = m.mass;
+  a.new_mass = m.new_mass;
+  a.ld = m.ld;
+  a.new_ld = m.new_ld;
+  a.words = (m.new_pages + 31) / 32;
+  a.read = static_cast<uint32_t*>(bitmaps);
+  a.written = a.read + a.words;
+  a.twice = a.written + a.words;
+  a.err = err;
+  cudaError_t e = launch_cluster("evict_mark", k_evict_mark, kCluster, kCluster, 1024, 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = ((int64_t)m.budget + kPage - 1) / kPage * s.batch;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  e = launch_pdl("evict_compact", k_evict_compact, dim3((unsigned)grid), dim3(kMoveThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  return counted(cudaGetLastError());
+}
+
+}  // namespace dsa

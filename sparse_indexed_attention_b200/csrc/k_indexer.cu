@@ -45,9 +45,8 @@
 // global memory, then writes its own selections, ascending, at offsets
 // derived from per-item counts.  Rows meet through arrival counters with
 // bounded waits; the persistent grid (one CTA per SM) is all resident.
-#include <cudaTypedefs.h>
-
 #include "sm100.cuh"
+#include "tensor_map.cuh"
 #include "topk_select.cuh"
 
 namespace dsa {
@@ -931,24 +930,12 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
 // ---------------------------------------------------------------- host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // Row-major 2-D map: rows of `row_elems` elements, box of box_x x box_y,
 // 128-byte swizzle (64-byte for the 64-byte rows of MXFP4 codes).
 bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint32_t box_x,
               uint32_t box_y) {
   const bool narrow = !bf16 && row_elems == 64;
-  auto fn = encode_fn();
+  auto fn = tensor_map_encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {row_elems, rows};
   const cuuint64_t strides[1] = {row_elems * (bf16 ? 2 : 1)};

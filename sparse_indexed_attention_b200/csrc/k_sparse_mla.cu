@@ -53,11 +53,9 @@
 // exactly: an E4M3 value times a power of two has at most 4 significant bits --
 // and store the same 16-byte pieces the bf16 gather would have copied; the
 // MMAs, softmax and epilogue are the bf16 path's.
-#include <cudaTypedefs.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
+#include "kv8.cuh"
 #include "sm100.cuh"
+#include "tensor_map.cuh"
 
 namespace dsa {
 
@@ -116,43 +114,6 @@ constexpr uint32_t IDESC_PV = make_idesc_major(true, kHG, 256, 0, 1);  // O += P
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;     // log2 units
-
-// 2^x from the MUFU unit (approximate, subnormal results flushed to 0;
-// ex2(-inf) = +0).
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 8 bytes from global memory through the read-only path.
-__device__ __forceinline__ uint2 ld_nc_v2(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
-// 2^(byte - 127) for a tile-scale byte, exact (2^-127 is the subnormal 0x00400000).
-__device__ __forceinline__ float tile_scale(uint32_t byte) {
-  return byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
-}
-
-// Eight E4M3 codes (little-endian: element k in byte k) times a power-of-two
-// scale, as eight bf16 (element 2i in the low half of word i).  Exact: an
-// E4M3 value is an fp16 value, and times 2^e it has at most 4 significant bits.
-__device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 codes, float sc) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? codes.x : codes.y;
-    const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)((w >> (16 * (i & 1))) & 0xFFFFu);
-    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-    o[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 __device__ __forceinline__ void store_out(void* out, bool f32, int64_t i, float v) {
   if (f32)
@@ -799,31 +760,6 @@ cudaError_t launch_attn(const CUtensorMap& tq, const AttnArgs& a, int64_t ctas, 
                     (size_t)C::SMEM, st, tq, a);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
-// bf16 [rows, 576] map with a box of 64 dims x 64 rows and the 128-byte swizzle.
-bool make_map_576(CUtensorMap* m, const void* base, uint64_t rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kDQK, rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kDQK * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)kHG};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 size_t sparse_mla_partials_bytes(int T, int K, int H) {
@@ -843,7 +779,7 @@ cudaError_t launch_sparse_mla(const SeqsDev& s, TokenMap tm, bool tm_early, cons
   float* part_o = reinterpret_cast<float*>(partials);
   float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)T * splits * H * kDV);
   CUtensorMap tq;
-  if (!make_map_576(&tq, q, (uint64_t)T * H)) return cudaErrorInvalidValue;
+  if (!make_bf16_rows_map(&tq, q, kDQK, (uint64_t)T * H, kHG)) return cudaErrorInvalidValue;
   const bool kv8 = kv8_scale != nullptr;
   AttnArgs a{s,
              tm,
