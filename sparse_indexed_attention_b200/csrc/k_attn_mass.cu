@@ -11,15 +11,20 @@
 // the columns (M = 128 rows, N = H heads, K = 576), so the sum over heads stays
 // inside one thread -- the transposed product of the attention kernel would
 // need a reduction over lanes -- and a row is gathered once for all heads.
-//   * eight loader warps resolve the slice's rows (index list -> page table ->
+//   * four loader warps resolve the slice's rows (index list -> page table ->
 //     pool row) and copy them, 128 rows x 64 dims (16 KB) at a time, into a ring of
 //     128-byte-swizzled operand slots, each with its own barriers: the query
 //     (H x 1152 bytes) fills most of shared memory, and the ring keeps loads in
 //     flight across blocks;
-//   * one thread issues the MMAs, four per slot, into one of two accumulators;
-//   * four warps read the other accumulator: p = 2^(c S - L_h), summed over h.
-//     c = scale log2 e and L = lse log2 e are used as two fp32 terms each: one
-//     would be off by 2^-24 of the logit, 1e-6 of p at logits of 16.
+//   * one thread issues the MMAs, four per slot, each slot's 64 dims into an
+//     accumulator of its own (a ring of four);
+//   * eight warps, two per lane quarter with half of the heads each, add the
+//     nine partial logits in registers and take p = 2^(c S - L_h), summed over h.
+// Precision.  The tensor core's fp32 additions truncate: one chain of 36
+// accumulations per logit was off by 3e-6 of the mass (an fp32 product rounded to
+// nearest: 6.5e-7), all one way.  Chains of four, added with rounding, are not.
+// c = scale log2 e and L = lse log2 e are used as two fp32 terms each: one would
+// be off by 2^-24 of the logit, 1e-6 of p at logits of 16.
 //
 // The sum over tokens is held in 64-bit fixed point (units of 2^-40 of one
 // token's whole attention, 8.4 million tokens before it overflows): integer
@@ -39,13 +44,17 @@ using namespace sm100;
 constexpr int kRows = 128;                   // rows per block (the MMA's M)
 constexpr int kAtoms = kDQK / 64;            // 9 slices of 64 dims
 constexpr int kSlotBytes = kRows * 128;
-constexpr int kLoaders = 256;                // warps 4-11
-constexpr int kLoaderBarrier = 1;
+constexpr int kSumWarps = 8;                 // warps 0-7
+constexpr int kLoaders = 128;                // warps 8-11
+constexpr int kLoaderBarrier = 1, kSumBarrier = 2;
 constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;            // warps 0-3 sum, 4-11 load, 12 issues MMAs and owns TMEM
-constexpr int kMaxSlots = 9;
-constexpr int kTmemCols = 256;               // two accumulators of up to 128 columns
+constexpr int kThreads = 13 * 32;            // warp 12 issues MMAs and owns TMEM
+constexpr int kMaxSlots = 8;
+constexpr int kAccs = 4;                     // accumulators of up to 128 columns
+constexpr int kTmemCols = 512;
 constexpr int kPerLoader = kMaxK / kLoaders;
+constexpr int kRowsPerLoader = kRows * 8 / kLoaders;  // a thread's 16-byte pieces of a slot
+constexpr int kAhead = 3;                    // FP8 cache: slots whose codes are loaded ahead (a divisor of kAtoms)
 
 struct MassArgs {
   SeqsDev s;
@@ -63,18 +72,28 @@ struct MassArgs {
 
 // Shared memory from a 1024-aligned base: query, ring, rows, lse, barriers.
 struct Layout {
-  int q_atom, ring, rows, lse, bars, total;
+  int q_atom, ring, rows, lse, half, bars, total;
   __host__ __device__ Layout(int H, int slots) {
     q_atom = H * 128;
     ring = kAtoms * q_atom;
     rows = ring + slots * kSlotBytes;
     lse = rows + kMaxK * 4;
-    bars = lse + 128 * 8;
-    total = bars + (2 * kMaxSlots + 8) * 8 + 16;
+    half = lse + 128 * 8;                  // [2] the second heads' sums of a block's rows
+    bars = half + 2 * kRows * 4;
+    total = bars + (2 * kMaxSlots + 2 * kAccs + 4) * 8 + 16;
   }
 };
 
-template <bool kKv8>
+// Two warpgroups meet at the block's sums: the second arrives with its half, the first waits.
+__device__ __forceinline__ void sums_arrive() {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kSumBarrier), "n"(kSumWarps * 32) : "memory");
+}
+__device__ __forceinline__ void sums_wait() {
+  asm volatile("barrier.cta.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumWarps * 32) : "memory");
+}
+
+// CH: chunks of 32 heads that a summing thread holds (two for H = 128).
+template <bool kKv8, int CH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -85,12 +104,12 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* full = bars;                       // [slots]
   uint64_t* empty = bars + kMaxSlots;          // [slots]
-  uint64_t* s_full = bars + 2 * kMaxSlots;     // [2]
-  uint64_t* s_empty = s_full + 2;              // [2]
-  uint64_t* q_full = s_empty + 2;
+  uint64_t* s_full = bars + 2 * kMaxSlots;     // [kAccs]
+  uint64_t* s_empty = s_full + kAccs;          // [kAccs]
+  uint64_t* q_full = s_empty + kAccs;
   uint64_t* ready = q_full + 1;                // rows and lse are in shared memory
   uint64_t* mma_drain = ready + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxSlots + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,9 +120,9 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       mbar_init(&full[i], kLoaders);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
+      mbar_init(&s_empty[i], kSumWarps);
     }
     mbar_init(q_full, 1);
     mbar_init(ready, 1);
@@ -124,15 +143,15 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   const TokenPlace at = locate_token(a.s, t);
   if (at.pos < 0 && threadIdx.x == 0) raise_error(a.err, kErrBadIndex);
   const int nblk = at.pos >= 0 && kend > kbeg ? (kend - kbeg + kRows - 1) / kRows : 0;
-  const int acc_cols = a.H < 32 ? 32 : a.H;
+  const int acc_cols = a.H < 64 ? 64 : a.H;
 
   if (threadIdx.x == kMmaWarp * 32 && nblk > 0) {
     mbar_arrive_expect_tx(q_full, (uint32_t)(kAtoms * L.q_atom));
     for (int i = 0; i < kAtoms; ++i) tma_load_2d(smem + i * L.q_atom, &tq, q_full, 64 * i, t * a.H);
   }
-  if (warp >= 4 && warp < kMmaWarp && nblk > 0) {
+  if (warp >= kSumWarps && warp < kMmaWarp && nblk > 0) {
     // ---------------------------------------------------------------- loaders
-    const int li = threadIdx.x - 128;
+    const int li = threadIdx.x - kSumWarps * 32;
     const int n = kend - kbeg;
     {
       int sidx[kPerLoader], page[kPerLoader];
@@ -169,48 +188,63 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
     }
     bool ok = !bar_red_or(kLoaderBarrier, kLoaders, false);
     if (li == 0) mbar_arrive(ready);
-    const int rsub = li >> 3, piece = li & 7;  // this thread's rows: rsub + 32 u, their 16-byte piece of each atom
+    const int rsub = li >> 3, piece = li & 7;  // this thread's rows: rsub + 16 u, their 16-byte piece of each atom
     const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)piece ^ ((uint32_t)rsub & 7u)) << 4);
     const uint32_t ring = smem_u32(smem + L.ring);
-    // FP8 cache: a block's codes are loaded one block ahead of their conversion
-    uint2 raw[4][kAtoms], scl[4];
-    auto load_block = [&](int j) {
+    // FP8 cache: codes pass through registers, loaded kAhead slots ahead of their conversion
+    constexpr int kRaw = kKv8 ? kRowsPerLoader : 1;
+    uint2 raw[kAhead][kRaw], scl[kRaw], scl_next[kRaw];
+    auto load_codes = [&](int j, int i, uint2 (&to)[kRaw]) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = rows[j * kRows + rsub + 32 * u];
-        const uint8_t* src = a.kv + (int64_t)(row < 0 ? 0 : row) * kDQK + 8 * piece;
-#pragma unroll
-        for (int i = 0; i < kAtoms; ++i) raw[u][i] = row >= 0 ? ld_nc_v2(src + 64 * i) : make_uint2(0u, 0u);
-        scl[u] = row >= 0 ? ld_nc_v2(a.kv_scale + (int64_t)row * 8) : make_uint2(0x7F7F7F7Fu, 0x7Fu);
+      for (int u = 0; u < kRaw; ++u) {
+        const int row = rows[j * kRows + rsub + 16 * u];
+        to[u] = row >= 0 ? ld_nc_v2(a.kv + (int64_t)row * kDQK + 64 * i + 8 * piece) : make_uint2(0u, 0u);
       }
     };
-    if constexpr (kKv8) load_block(0);
+    auto load_scales = [&](int j, uint2 (&to)[kRaw]) {
+#pragma unroll
+      for (int u = 0; u < kRaw; ++u) {
+        const int row = rows[j * kRows + rsub + 16 * u];
+        to[u] = row >= 0 ? ld_nc_v2(a.kv_scale + (int64_t)row * 8) : make_uint2(0x7F7F7F7Fu, 0x7Fu);
+      }
+    };
+    if constexpr (kKv8) {
+      load_scales(0, scl);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load_codes(0, i, raw[i]);
+    }
     int slot = 0, phase = 0;
     for (int j = 0; j < nblk && ok; ++j) {
-      int row[4];
+      int row[kRowsPerLoader];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) row[u] = rows[j * kRows + rsub + 32 * u];
+      for (int u = 0; u < kRowsPerLoader; ++u) row[u] = rows[j * kRows + rsub + 16 * u];
 #pragma unroll
       for (int i = 0; i < kAtoms; ++i) {
         ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
         if (ok) {
           if constexpr (kKv8) {
             uint8_t* dst = smem + L.ring + slot * kSlotBytes + swz;
+            const int tile = i >> 1;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int tile = i >> 1;
+            for (int u = 0; u < kRaw; ++u) {
               const uint32_t byte = (tile < 4 ? (scl[u].x >> (8 * tile)) : scl[u].y) & 0xFFu;
-              *reinterpret_cast<uint4*>(dst + u * 4096) = e4m3x8_to_bf16x8(raw[u][i], tile_scale(byte));
+              *reinterpret_cast<uint4*>(dst + u * 2048) = e4m3x8_to_bf16x8(raw[i % kAhead][u], tile_scale(byte));
             }
             fence_proxy_async_smem();  // the MMAs read these stores through the async proxy
             mbar_arrive(&full[slot]);
+            if (i + kAhead < kAtoms) {
+              load_codes(j, i + kAhead, raw[i % kAhead]);
+            } else if (j + 1 < nblk) {
+              if (i + kAhead == kAtoms) load_scales(j + 1, scl_next);
+              load_codes(j + 1, i + kAhead - kAtoms, raw[i % kAhead]);
+            }
           } else {
             const uint32_t dst = ring + slot * kSlotBytes + swz;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kRowsPerLoader; ++u) {
               const bool live = row[u] >= 0;
               const uint8_t* src = a.kv + (live ? (int64_t)row[u] * (kDQK * 2) : 0) + 128 * i + 16 * piece;
-              cp_async_16_zfill(dst + u * 4096, src, live ? 16u : 0u);
+              cp_async_16_zfill(dst + u * 2048, src, live ? 16u : 0u);
             }
             cp_async_mbar_arrive(&full[slot]);  // counts once this thread's copies land
           }
@@ -221,7 +255,8 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
         }
       }
       if constexpr (kKv8) {
-        if (ok && j + 1 < nblk) load_block(j + 1);
+#pragma unroll
+        for (int u = 0; u < kRaw; ++u) scl[u] = scl_next[u];
       }
     }
     if (!ok) *abort_flag = 1;
@@ -232,28 +267,30 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
     if (lane == 0) {
       const uint32_t idesc = make_idesc(true, kRows, a.H);
       bool ok = mbar_wait(q_full, 0, a.err, a.wait_ns);
-      int slot = 0, phase = 0;
+      int slot = 0, phase = 0, acc = 0, aphase = 0;
       for (int j = 0; j < nblk && ok; ++j) {
-        const int acc = j & 1;
-        ok = !*abort_flag && mbar_wait(&s_empty[acc], ((j >> 1) & 1) ^ 1, a.err, a.wait_ns);
-        tc_fence_after();
-        for (int i = 0; i < kAtoms && ok; ++i) {
-          ok = mbar_wait(&full[slot], phase, a.err, a.wait_ns);
+        for (int i = 0; i < kAtoms; ++i) {
+          ok = !*abort_flag && mbar_wait(&full[slot], phase, a.err, a.wait_ns) &&
+               mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns);
           if (!ok) break;
-          fence_proxy_async_smem();  // written by cp.async (generic proxy)
+          fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
           tc_fence_after();
           const uint32_t ab = smem_u32(smem + L.ring + slot * kSlotBytes), bb = smem_u32(smem + i * L.q_atom);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ss<true>(tmem + acc * acc_cols, sw128_kmajor_desc(ab + kk * 32), sw128_kmajor_desc(bb + kk * 32), idesc,
-                         (i | kk) != 0);
+                         kk != 0);
           mma_commit(&empty[slot]);
+          mma_commit(&s_full[acc]);
           if (++slot == a.slots) {
             slot = 0;
             phase ^= 1;
           }
+          if (++acc == kAccs) {
+            acc = 0;
+            aphase ^= 1;
+          }
         }
-        if (ok) mma_commit(&s_full[acc]);
       }
       if (!ok) *abort_flag = 1;
       // drain, also after a failed wait: the query's copy has landed and no MMA
@@ -263,40 +300,65 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       mbar_wait(mma_drain, 0, a.err, kDrainLimitNs);
     }
     __syncwarp();
-  } else if (warp < 4 && nblk > 0) {
+  } else if (warp < kSumWarps && nblk > 0) {
     // ---------------------------------------------------------------- sums
-    const int r = threadIdx.x;
-    const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    const int wg = warp >> 2, r = threadIdx.x & 127;  // half of the heads, row of the block
+    const int heads = a.H >> 1, h0 = wg * heads;
+    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h0;
     const float inv_h = 1.f / (float)a.H;  // a power of two
+    float* other = reinterpret_cast<float*>(smem + L.half);
     bool ok = __all_sync(0xffffffffu, mbar_wait(ready, 0, a.err, a.wait_ns));
-    for (int j = 0; j < nblk && ok; ++j) {
-      const int acc = j & 1, k = j * kRows + r;
-      const bool live = rows[k] >= 0;
+    int acc = 0, aphase = 0;
+    for (int j = 0; j < nblk; ++j) {
+      const int k = j * kRows + r;
+      const bool live = ok && rows[k] >= 0;
       const int s = live ? __ldg(a.idx + (int64_t)t * a.K + kbeg + k) : 0;
-      ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[acc], (j >> 1) & 1, a.err, a.wait_ns));
-      if (!ok) break;
-      tc_fence_after();
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < a.H; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(t_lane + acc * acc_cols + c, v);
-        tmem_ld_wait_regs(v);
+      float x[CH][32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 lh = lse[c + i];
-          const float x = __uint_as_float(v[i]);
-          const float p = ex2_ftz(fmaf(x, a.c_hi, -lh.x) + fmaf(x, a.c_lo, -lh.y));
-          if (c + i < a.H) sum[i & 3] += p;  // H = 16 fills half a chunk
+      for (int i = 0; i < kAtoms; ++i) {
+        ok = ok && __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[acc], aphase, a.err, a.wait_ns));
+        if (ok) {
+          tc_fence_after();
+          uint32_t v[CH][32];  // fewer than 32 heads: the other columns are read and left out below
+#pragma unroll
+          for (int c = 0; c < CH; ++c) tmem_ld32(t_lane + acc * acc_cols + 32 * c, v[c]);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            tmem_ld_wait_regs(v[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c][e] = i == 0 ? __uint_as_float(v[c][e]) : x[c][e] + __uint_as_float(v[c][e]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[acc]);
+        }
+        if (++acc == kAccs) {
+          acc = 0;
+          aphase ^= 1;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[acc]);
-      const float w = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * inv_h;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 lh = lse[h0 + 32 * c + e];
+          const float p = ex2_ftz(fmaf(x[c][e], a.c_hi, -lh.x) + fmaf(x[c][e], a.c_lo, -lh.y));
+          if (32 * c + e < heads) sum[e & 3] += p;
+        }
+      float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // the second half's sum goes through shared memory, two buffers: the ring of
+      // accumulators lets no warp run a whole block ahead of another
+      if (wg == 1) {
+        other[(j & 1) * kRows + r] = w;
+        sums_arrive();
+        continue;
+      }
+      sums_wait();
+      w = (w + other[(j & 1) * kRows + r]) * inv_h;
       // a NaN (from a NaN or an lse that does not belong to these logits) adds nothing
       const float lim = w > 0.f ? fminf(w, 1.f) : 0.f;
-      if (live && lim > 0.f)
+      if (ok && live && lim > 0.f)
         atomicAdd(a.mass + (int64_t)at.seq * a.ld + s, (unsigned long long)__float2ll_rn(lim * 0x1p40f));
     }
     if (!ok) *abort_flag = 1;
@@ -329,17 +391,17 @@ int mass_splits(int T, int K) {
   return best;
 }
 
-template <bool kKv8>
+template <bool kKv8, int CH>
 cudaError_t launch(const CUtensorMap& tq, const MassArgs& a, int64_t ctas, cudaStream_t st) {
   static thread_local int attr_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (attr_dev != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_mass<kKv8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(k_attn_mass<kKv8, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     attr_dev = dev;
   }
-  return launch_pdl("attn_mass", k_attn_mass<kKv8>, dim3((unsigned)ctas), dim3(kThreads),
+  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(kThreads),
                     (size_t)(Layout(a.H, a.slots).total + 1024), st, tq, a);
 }
 
@@ -359,7 +421,8 @@ cudaError_t launch_attn_mass(const SeqsDev& s, const __nv_bfloat16* q, const voi
              ld, K, H, per * kRows, splits, H == 128 ? 4 : kMaxSlots, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
   const int64_t ctas = (int64_t)s.num_tokens * splits;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaError_t e = kv8_scale ? launch<true>(tq, a, ctas, st) : launch<false>(tq, a, ctas, st);
+  cudaError_t e = H == 128 ? (kv8_scale ? launch<true, 2>(tq, a, ctas, st) : launch<false, 2>(tq, a, ctas, st))
+                           : (kv8_scale ? launch<true, 1>(tq, a, ctas, st) : launch<false, 1>(tq, a, ctas, st));
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }
