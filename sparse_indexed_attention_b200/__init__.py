@@ -128,11 +128,12 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The device's current stream, as the integer that ctypes passes on."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class _Nothing:
@@ -161,17 +162,21 @@ def _need(t, name: str, dtypes, shape, device: torch.device, min_rows: int = 0):
     otherwise be read out of bounds."""
     try:  # fast path: one pass over the metadata, no message building
         sz = t.shape
-        ok = t.device == device and t.dtype in dtypes and len(sz) == len(shape) and sz[0] >= min_rows \
-            and t.is_contiguous()
-        if ok:
-            for g, w in zip(sz, shape):
-                if w is not None and g != w:
-                    ok = False
-                    break
+        if t.dtype in dtypes and t.device == device and t.is_contiguous() and sz[0] >= min_rows \
+                and (sz == shape or _fits(sz, shape)):
+            return
     except (AttributeError, IndexError):
-        ok = False
-    if not ok:
-        _refuse(t, name, dtypes, shape, device, min_rows)
+        pass
+    _refuse(t, name, dtypes, shape, device, min_rows)
+
+
+def _fits(sz, shape) -> bool:
+    if len(sz) != len(shape):
+        return False
+    for g, w in zip(sz, shape):
+        if w is not None and g != w:
+            return False
+    return True
 
 
 def _refuse(t, name, dtypes, shape, device, min_rows):
@@ -315,8 +320,9 @@ def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     During stream capture a buffer that is not cached yet belongs to the graph
     alone (its zeroing is part of the graph and has not run), so it is not
     cached; a captured call whose error flag is to be read passes its own."""
-    device = torch.device(device)
-    if device.type == "cuda" and device.index is None:
+    if not isinstance(device, torch.device):
+        device = torch.device(device)
+    if device.index is None and device.type == "cuda":
         device = torch.device("cuda", torch.cuda.current_device())
     k = (device, key)
     ws = _ws_cache.get(k)
@@ -430,8 +436,9 @@ def dsa_index_scores(seqs: Seqs, qI, w, kI, kI_scale=None, scores=None, ld=None,
     need = _lib.dsa_workspace_size(DSA_OP_INDEX_SCORES, ctypes.byref(c), 1, 16)
     ws = ws if ws is not None else workspace(need, qI.device, "index_scores")
     _need_ws(ws, dev)
-    _check(_lib.dsa_index_scores(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype, _ptr(scores),
-                                 ld, _ptr(ws), ws.numel(), _stream(qI.device)), "dsa_index_scores")
+    with _on(dev):
+        _check(_lib.dsa_index_scores(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype,
+                                     _ptr(scores), ld, _ptr(ws), ws.numel(), _stream(dev)), "dsa_index_scores")
     return scores
 
 
@@ -527,11 +534,12 @@ def dsa_index_topk_attn(seqs: Seqs, qI, w, kI, kI_scale, q, kv, K: int, scale: f
     _need_ws(ws, dev)
     ev = None if q_ready is None else ctypes.c_void_p(q_ready.cuda_event)
     kv_dtype = DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3
-    _check(_lib.dsa_index_topk_attn_ex(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype, _ptr(q),
-                                       _ptr(kv), _ptr(kv_scale), kv_dtype, K, H, scale, _ptr(out), _out_dtype(out),
-                                       _ptr(lse), _ptr(idx_out), _ptr(ws), ws.numel(),
-                                       DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev, _stream(q.device)),
-           "dsa_index_topk_attn")
+    with _on(dev):
+        _check(_lib.dsa_index_topk_attn_ex(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype,
+                                           _ptr(q), _ptr(kv), _ptr(kv_scale), kv_dtype, K, H, scale, _ptr(out),
+                                           _out_dtype(out), _ptr(lse), _ptr(idx_out), _ptr(ws), ws.numel(),
+                                           DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev, _stream(dev)),
+               "dsa_index_topk_attn")
     return out, lse
 
 
@@ -613,15 +621,15 @@ def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=No
     new_pages = None
     for i, p in enumerate(pools):
         src, dst = p if isinstance(p, (tuple, list)) else (p, p)
-        for t, name in ((src, f"pools[{i}]"), (dst, f"pools[{i}] destination")):
+        for t in (src,) if dst is src else (src, dst):
             if not isinstance(t, torch.Tensor) or t.dim() < 1:
-                raise TypeError(f"{name}: expected a tensor of rows")
-            _need(t, name, (src.dtype,), (None, *src.shape[1:]), dev)
-        if src.shape[0] < pages * 64:
-            raise ValueError(f"pools[{i}]: {src.shape[0]} rows, the page pool needs at least {pages * 64}")
-        if dst.shape[0] < 64:
-            raise ValueError(f"pools[{i}] destination: less than a page of rows")
-        here = pages if dst is src else dst.shape[0] // 64
+                raise TypeError(f"pools[{i}]: expected a tensor of rows")
+        row = src.shape[1:]
+        _need(src, f"pools[{i}]", (src.dtype,), (src.shape[0], *row), dev, pages * 64)
+        here = pages
+        if dst is not src:
+            _need(dst, f"pools[{i}] destination", (src.dtype,), (dst.shape[0], *row), dev, 64)
+            here = dst.shape[0] // 64
         new_pages = here if new_pages is None else min(new_pages, here)
         cp[i].src, cp[i].dst = src.data_ptr(), dst.data_ptr()
         cp[i].row_bytes = src.numel() // src.shape[0] * src.element_size()

@@ -16,10 +16,20 @@
 //     128-byte-swizzled operand slots, each with its own barriers: the query
 //     (H x 1152 bytes) fills most of shared memory, and the ring keeps loads in
 //     flight across blocks;
-//   * one thread issues the MMAs, four per slot, each slot's 64 dims into an
-//     accumulator of its own (a ring of four);
+//   * three threads, each taking every third slot, issue the MMAs, four per
+//     slot, each slot's 64 dims into an accumulator of its own (a ring of four): one
+//     thread's waits, fence, issue and commits of a slot are a serial 900 cycles, three
+//     times what the slot's rows take to arrive;
 //   * eight warps, two per lane quarter with half of the heads each, add the
 //     nine partial logits in registers and take p = 2^(c S - L_h), summed over h.
+// FP8 cache.  Its codes become fp16, one conversion instruction per pair and exact;
+// their tiles' scales, powers of two per row, multiply the partial logits instead
+// (a tile is two slots), in the thread that owns the row.  The query becomes fp16 as
+// well, each head times the power of two that brings its largest value to 2^14:
+// values 2^-28 of that and less lose bits, 2^-39 of the largest at most.  (As bf16
+// the codes cost five times the instructions, and that bounded the kernel: 106 us
+// where the bf16 cache takes 47.)  A CTA takes 64 heads then, which leaves shared
+// memory for the staged codes and registers for twice the loader warps.
 // Precision.  The tensor core's fp32 additions truncate: one chain of 36
 // accumulations per logit was off by 3e-6 of the mass (an fp32 product rounded to
 // nearest: 6.5e-7), all one way.  Chains of four, added with rounding, are not.
@@ -45,16 +55,14 @@ constexpr int kRows = 128;                   // rows per block (the MMA's M)
 constexpr int kAtoms = kDQK / 64;            // 9 slices of 64 dims
 constexpr int kSlotBytes = kRows * 128;
 constexpr int kSumWarps = 8;                 // warps 0-7
-constexpr int kLoaders = 128;                // warps 8-11
+constexpr int kIssuers = 3;                  // warps 8-10, one thread each; warp 8 owns TMEM
 constexpr int kLoaderBarrier = 1, kSumBarrier = 2;
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;            // warp 12 issues MMAs and owns TMEM
+constexpr int kMmaWarp = kSumWarps;
+constexpr int kLoadWarp = kMmaWarp + kIssuers;
 constexpr int kMaxSlots = 8;
 constexpr int kAccs = 4;                     // accumulators of up to 128 columns
 constexpr int kTmemCols = 512;
-constexpr int kPerLoader = kMaxK / kLoaders;
-constexpr int kRowsPerLoader = kRows * 8 / kLoaders;  // a thread's 16-byte pieces of a slot
-constexpr int kAhead = 3;                    // FP8 cache: slots whose codes are loaded ahead (a divisor of kAtoms)
+static_assert(kAtoms % kIssuers == 0, "each issuer takes the same atoms of every block");
 
 struct MassArgs {
   SeqsDev s;
@@ -64,60 +72,114 @@ struct MassArgs {
   const float* lse;
   unsigned long long* mass;
   int64_t ld;
-  int K, H, ks, splits, slots;
+  int K, H, hg, ks, splits, slots;  // hg heads per CTA
   float c_hi, c_lo;          // scale * log2(e) as two terms
   uint32_t* err;
   uint64_t wait_ns;
 };
 
-// Shared memory from a 1024-aligned base: query, ring, rows, lse, barriers.
+// Shared memory from a 1024-aligned base: query, ring, staged codes, rows, lse, barriers.
 struct Layout {
-  int q_atom, ring, rows, lse, half, bars, total;
-  __host__ __device__ Layout(int H, int slots) {
+  int q_atom, ring, stage, rows, head, bars, total;
+  __host__ __device__ Layout(int H, int slots, int ahead, int ks) {
     q_atom = H * 128;
     ring = kAtoms * q_atom;
-    rows = ring + slots * kSlotBytes;
-    lse = rows + kMaxK * 4;
-    half = lse + 128 * 8;                  // [2] the second heads' sums of a block's rows
-    bars = half + 2 * kRows * 4;
-    total = bars + (2 * kMaxSlots + 2 * kAccs + 4) * 8 + 16;
+    stage = ring + slots * kSlotBytes;
+    rows = stage + ahead * (kSlotBytes / 2);
+    head = rows + ks * 4;                  // and 32 entries more: chunks of 32 heads are read whole
+    bars = head + H * 16 + 512;
+    total = bars + (2 * kMaxSlots + 2 * kAccs + 5) * 8 + 16;
   }
 };
 
-// Two warpgroups meet at the block's sums: the second arrives with its half, the first waits.
-__device__ __forceinline__ void sums_arrive() {
-  asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kSumBarrier), "n"(kSumWarps * 32) : "memory");
-}
-__device__ __forceinline__ void sums_wait() {
+// A barrier of the summing warps.
+__device__ __forceinline__ void sums_sync() {
   asm volatile("barrier.cta.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumWarps * 32) : "memory");
 }
 
+// FP8 cache: the query tile in shared memory from bf16 to fp16, in place, by the
+// summing warps.  256 / heads neighbouring threads share a head; its factor becomes
+// scale log2(e) / 2^s with s the power that was multiplied in.
+__device__ __forceinline__ void query_to_f16(uint8_t* q, int q_atom, int heads, float c_hi, float c_lo, float4* head) {
+  const int per = kSumWarps * 32 / heads;        // threads per head: 4, 8 or 16
+  const int h = threadIdx.x / per, sub = threadIdx.x % per;
+  const int chunks = kAtoms * 8;                 // 16-byte pieces of a head
+  uint32_t m = 0;
+  for (int k = sub; k < chunks; k += per) {
+    const uint4 v = *reinterpret_cast<const uint4*>(q + (k >> 3) * q_atom + h * 128 + (k & 7) * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  }
+  for (int o = 1; o < per; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // largest value to [2^14, 2^15); zero, infinite and NaN heads keep their scale
+  int s = m == 0u || m >= 0x7F80u ? 0 : 141 - (int)(m >> 7);
+  s = min(s, 126);
+  const float up = __uint_as_float((uint32_t)(127 + s) << 23), down = __uint_as_float((uint32_t)(127 - s) << 23);
+  for (int k = sub; k < chunks; k += per) {
+    uint4* at = reinterpret_cast<uint4*>(q + (k >> 3) * q_atom + h * 128 + (k & 7) * 16);
+    uint4 v = *at;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 r = __floats2half2_rn(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+      w[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (sub == 0) {
+    head[h].z = c_hi * down;
+    head[h].w = c_lo * down;
+  }
+}
+
+// Operand slots and staged FP8 codes (8 KB per atom) share what the query leaves.
+template <bool kKv8, int CH>
+struct Roles {
+  static_assert(!kKv8 || CH == 1, "FP8 cache: up to 64 heads per CTA");
+  static constexpr int groups = kKv8 ? kIssuers : 1;  // loader groups, taking atoms in turn
+  static constexpr int loaders = kKv8 ? 64 * groups : 128;
+  static constexpr int threads = 32 * kLoadWarp + loaders;
+  // A barrier's parity tells its next phase from this one, not from the one after, so
+  // nobody may wait for a slot two uses ahead.  A loader waits for its slot's release in
+  // the order of uses: alone, or (groups) because a slot always comes back to the same
+  // group.  An issuer waits for its accumulator first, whose release says that every
+  // atom up to the fourth before was summed, so the slot's earlier use is over.
+  static constexpr int slots = kKv8 ? 6 : (CH == 2 ? 4 : 8);
+  static_assert(slots % groups == 0 && slots >= kAccs && slots <= kMaxSlots && kAccs > kIssuers, "see above");
+  static constexpr int ahead = kKv8 ? 2 : 0;     // atoms that a group stages ahead
+};
+
 // CH: chunks of 32 heads that a summing thread holds (two for H = 128).
 template <bool kKv8, int CH>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<kKv8, CH>::threads, 1)
 k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
+  constexpr int kLoaders = Roles<kKv8, CH>::loaders;
+  constexpr int kPerLoader = (kMaxK + kLoaders - 1) / kLoaders;  // list entries a loader resolves
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const Layout L(a.H, a.slots);
+  const Layout L(a.hg, a.slots, Roles<kKv8, CH>::ahead * Roles<kKv8, CH>::groups, a.ks);
   int32_t* rows = reinterpret_cast<int32_t*>(smem + L.rows);       // pool row of each slot of the slice, -1 = none
-  float2* lse = reinterpret_cast<float2*>(smem + L.lse);           // lse * log2(e) per head, two terms
+  float4* head = reinterpret_cast<float4*>(smem + L.head);          // per head: lse * log2(e), the logit's factor; two terms each
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* full = bars;                       // [slots]
   uint64_t* empty = bars + kMaxSlots;          // [slots]
   uint64_t* s_full = bars + 2 * kMaxSlots;     // [kAccs]
   uint64_t* s_empty = s_full + kAccs;          // [kAccs]
   uint64_t* q_full = s_empty + kAccs;
-  uint64_t* ready = q_full + 1;                // rows and lse are in shared memory
+  uint64_t* q_half = q_full + 1;               // FP8 cache: the query is fp16
+  uint64_t* ready = q_half + 1;                // rows and lse are in shared memory
   uint64_t* mma_drain = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x / a.splits, sp = blockIdx.x % a.splits;
+  const int groups = a.H / a.hg, unit = blockIdx.x / groups, head0 = (blockIdx.x % groups) * a.hg;
+  const int t = unit / a.splits, sp = unit % a.splits;
   const int kbeg = sp * a.ks, kend = min(a.K, kbeg + a.ks);
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.slots; ++i) {
-      mbar_init(&full[i], kLoaders);
+      mbar_init(&full[i], kKv8 ? kLoaders / 32 / Roles<kKv8, CH>::groups : kLoaders);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kAccs; ++i) {
@@ -125,8 +187,9 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       mbar_init(&s_empty[i], kSumWarps);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_half, kSumWarps);
     mbar_init(ready, 1);
-    mbar_init(mma_drain, 1);
+    mbar_init(mma_drain, kIssuers);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -143,15 +206,15 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   const TokenPlace at = locate_token(a.s, t);
   if (at.pos < 0 && threadIdx.x == 0) raise_error(a.err, kErrBadIndex);
   const int nblk = at.pos >= 0 && kend > kbeg ? (kend - kbeg + kRows - 1) / kRows : 0;
-  const int acc_cols = a.H < 64 ? 64 : a.H;
+  const int acc_cols = a.hg < 64 ? 64 : a.hg;
 
   if (threadIdx.x == kMmaWarp * 32 && nblk > 0) {
     mbar_arrive_expect_tx(q_full, (uint32_t)(kAtoms * L.q_atom));
-    for (int i = 0; i < kAtoms; ++i) tma_load_2d(smem + i * L.q_atom, &tq, q_full, 64 * i, t * a.H);
+    for (int i = 0; i < kAtoms; ++i) tma_load_2d(smem + i * L.q_atom, &tq, q_full, 64 * i, t * a.H + head0);
   }
-  if (warp >= kSumWarps && warp < kMmaWarp && nblk > 0) {
+  if (warp >= kLoadWarp && nblk > 0) {
     // ---------------------------------------------------------------- loaders
-    const int li = threadIdx.x - kSumWarps * 32;
+    const int li = threadIdx.x - kLoadWarp * 32;
     const int n = kend - kbeg;
     {
       int sidx[kPerLoader], page[kPerLoader];
@@ -177,119 +240,142 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
           raise_error(a.err, kErrBadIndex);
         if (k < nblk * kRows) rows[k] = row;
       }
-      if (li < a.H) {
-        const float v = __ldg(a.lse + (int64_t)t * a.H + li);
+      if (li < a.hg) {
+        const float v = __ldg(a.lse + (int64_t)t * a.H + head0 + li);
         constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266175e-8f;
         const float hi = v * kLog2e;
         // an infinite lse keeps its sign; its low term would be NaN
         const float lo = isinf(v) ? 0.f : fmaf(v, kLog2eLo, fmaf(v, kLog2e, -hi));
-        lse[li] = make_float2(hi, lo);
+        if constexpr (kKv8)  // the factors follow from the query's scale
+          *reinterpret_cast<float2*>(head + li) = make_float2(hi, lo);
+        else
+          head[li] = make_float4(hi, lo, a.c_hi, a.c_lo);
       }
     }
     bool ok = !bar_red_or(kLoaderBarrier, kLoaders, false);
     if (li == 0) mbar_arrive(ready);
-    const int rsub = li >> 3, piece = li & 7;  // this thread's rows: rsub + 16 u, their 16-byte piece of each atom
-    const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)piece ^ ((uint32_t)rsub & 7u)) << 4);
     const uint32_t ring = smem_u32(smem + L.ring);
-    // FP8 cache: codes pass through registers, loaded kAhead slots ahead of their conversion
-    constexpr int kRaw = kKv8 ? kRowsPerLoader : 1;
-    uint2 raw[kAhead][kRaw], scl[kRaw], scl_next[kRaw];
-    auto load_codes = [&](int j, int i, uint2 (&to)[kRaw]) {
-#pragma unroll
-      for (int u = 0; u < kRaw; ++u) {
-        const int row = rows[j * kRows + rsub + 16 * u];
-        to[u] = row >= 0 ? ld_nc_v2(a.kv + (int64_t)row * kDQK + 64 * i + 8 * piece) : make_uint2(0u, 0u);
-      }
-    };
-    auto load_scales = [&](int j, uint2 (&to)[kRaw]) {
-#pragma unroll
-      for (int u = 0; u < kRaw; ++u) {
-        const int row = rows[j * kRows + rsub + 16 * u];
-        to[u] = row >= 0 ? ld_nc_v2(a.kv_scale + (int64_t)row * 8) : make_uint2(0x7F7F7F7Fu, 0x7Fu);
-      }
-    };
-    if constexpr (kKv8) {
-      load_scales(0, scl);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) load_codes(0, i, raw[i]);
-    }
     int slot = 0, phase = 0;
-    for (int j = 0; j < nblk && ok; ++j) {
-      int row[kRowsPerLoader];
+    if constexpr (!kKv8) {
+      // thread: rows rsub + kStep u, their 16-byte piece of each atom
+      constexpr int kUnits = kRows * 8 / kLoaders, kStep = kLoaders / 8;
+      const int rsub = li >> 3, piece = li & 7;
+      const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)piece ^ ((uint32_t)rsub & 7u)) << 4);
+      for (int j = 0; j < nblk && ok; ++j) {
+        int row[kUnits];
 #pragma unroll
-      for (int u = 0; u < kRowsPerLoader; ++u) row[u] = rows[j * kRows + rsub + 16 * u];
+        for (int u = 0; u < kUnits; ++u) row[u] = rows[j * kRows + rsub + kStep * u];
 #pragma unroll
-      for (int i = 0; i < kAtoms; ++i) {
-        ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
-        if (ok) {
-          if constexpr (kKv8) {
-            uint8_t* dst = smem + L.ring + slot * kSlotBytes + swz;
-            const int tile = i >> 1;
-#pragma unroll
-            for (int u = 0; u < kRaw; ++u) {
-              const uint32_t byte = (tile < 4 ? (scl[u].x >> (8 * tile)) : scl[u].y) & 0xFFu;
-              *reinterpret_cast<uint4*>(dst + u * 2048) = e4m3x8_to_bf16x8(raw[i % kAhead][u], tile_scale(byte));
-            }
-            fence_proxy_async_smem();  // the MMAs read these stores through the async proxy
-            mbar_arrive(&full[slot]);
-            if (i + kAhead < kAtoms) {
-              load_codes(j, i + kAhead, raw[i % kAhead]);
-            } else if (j + 1 < nblk) {
-              if (i + kAhead == kAtoms) load_scales(j + 1, scl_next);
-              load_codes(j + 1, i + kAhead - kAtoms, raw[i % kAhead]);
-            }
-          } else {
+        for (int i = 0; i < kAtoms; ++i) {
+          ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
+          if (ok) {
             const uint32_t dst = ring + slot * kSlotBytes + swz;
 #pragma unroll
-            for (int u = 0; u < kRowsPerLoader; ++u) {
+            for (int u = 0; u < kUnits; ++u) {
               const bool live = row[u] >= 0;
               const uint8_t* src = a.kv + (live ? (int64_t)row[u] * (kDQK * 2) : 0) + 128 * i + 16 * piece;
-              cp_async_16_zfill(dst + u * 2048, src, live ? 16u : 0u);
+              cp_async_16_zfill(dst + u * kStep * 128, src, live ? 16u : 0u);
             }
             cp_async_mbar_arrive(&full[slot]);  // counts once this thread's copies land
           }
-        }
-        if (++slot == a.slots) {
-          slot = 0;
-          phase ^= 1;
+          if (++slot == a.slots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      if constexpr (kKv8) {
+    } else {
+      // Group g of 64 threads takes atoms g, g + 3, ...: the waits, fence and barrier of
+      // an atom cost each warp as much as its conversions.  Thread: rows rsub + 16 u, 16
+      // codes each.  They come kAhead of the group's atoms early into a place of the
+      // thread's own (no barrier), are converted and stored where the bf16 gather
+      // would have put the values.  A row that is not live reads row 0 of the pool:
+      // its logits, in a lane of their own, are not used.
+      using R = Roles<kKv8, CH>;
+      constexpr int kGroup = kLoaders / R::groups, kUnits = kRows * 4 / kGroup, kAhead = R::ahead;
+      static_assert(kGroup == 64 && kUnits == 8, "16 rows per step");
+      const int g = li / kGroup, lt = li % kGroup, rsub = lt >> 2, piece = lt & 3;
+      uint8_t* stage = smem + L.stage + g * (kAhead * kSlotBytes / 2) + lt * 16;
+      const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)(2 * piece) ^ ((uint32_t)rsub & 7u)) << 4);
+      const int total = nblk * kAtoms;
+      int next = g, next_place = 0;  // the next atom to fetch and its place
+      auto fetch = [&]() {
+        if (next < total) {
+          const int j = next / kAtoms, i = next - j * kAtoms;
+          const uint8_t* src = a.kv + 64 * i + 16 * piece;
+          const int32_t* rj = rows + j * kRows + rsub;
 #pragma unroll
-        for (int u = 0; u < kRaw; ++u) scl[u] = scl_next[u];
+          for (int u = 0; u < kUnits; ++u)
+            cp_async_16(stage + (next_place * kUnits + u) * (kGroup * 16), src + (int64_t)max(rj[16 * u], 0) * kDQK);
+          next += R::groups;
+          if (++next_place == kAhead) next_place = 0;
+        }
+        cp_async_commit();
+      };
+      for (int i = 0; i < kAhead; ++i) fetch();
+      int place = 0;
+      slot = g;  // a.slots exceeds the groups
+      for (int it = g; it < total; it += R::groups) {
+        cp_async_wait<kAhead - 1>();  // this thread's codes of the atom are in place
+        uint4 c[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+          c[u] = *reinterpret_cast<const uint4*>(stage + (place * kUnits + u) * (kGroup * 16));
+        if (++place == kAhead) place = 0;
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns));
+        if (!ok) break;
+        uint8_t* dst = smem + L.ring + slot * kSlotBytes;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          *reinterpret_cast<uint4*>(dst + swz + u * 2048) = e4m3x8_to_f16x8(make_uint2(c[u].x, c[u].y));
+          *reinterpret_cast<uint4*>(dst + (swz ^ 16u) + u * 2048) = e4m3x8_to_f16x8(make_uint2(c[u].z, c[u].w));
+        }
+        fence_proxy_async_smem();  // the MMAs read these stores through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+        fetch();
+        slot += R::groups;
+        if (slot >= a.slots) {
+          slot -= a.slots;
+          phase ^= 1;
+        }
       }
     }
     if (!ok) *abort_flag = 1;
     cp_async_wait_all();  // nothing this thread copies is still in flight at exit
     __syncwarp();
-  } else if (warp == kMmaWarp && nblk > 0) {
-    // ---------------------------------------------------------------- MMA issuer
+  } else if (warp >= kMmaWarp && warp < kLoadWarp && nblk > 0) {
+    // ---------------------------------------------------------------- MMA issuers
     if (lane == 0) {
-      const uint32_t idesc = make_idesc(true, kRows, a.H);
-      bool ok = mbar_wait(q_full, 0, a.err, a.wait_ns);
-      int slot = 0, phase = 0, acc = 0, aphase = 0;
-      for (int j = 0; j < nblk && ok; ++j) {
-        for (int i = 0; i < kAtoms; ++i) {
-          ok = !*abort_flag && mbar_wait(&full[slot], phase, a.err, a.wait_ns) &&
-               mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns);
-          if (!ok) break;
-          fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
-          tc_fence_after();
-          const uint32_t ab = smem_u32(smem + L.ring + slot * kSlotBytes), bb = smem_u32(smem + i * L.q_atom);
+      const uint32_t idesc = make_idesc(!kKv8, kRows, a.hg);  // bf16 or (FP8 cache) fp16 operands
+      bool ok = mbar_wait(kKv8 ? q_half : q_full, 0, a.err, a.wait_ns);
+      if constexpr (kKv8) fence_proxy_async_smem();  // the query was rewritten by the summing warps
+      int i = warp - kMmaWarp;  // atom of the block
+      int slot = i, phase = 0;  // a.slots and kAccs exceed kIssuers
+      int acc = i, aphase = 0;
+      for (int it = i; it < nblk * kAtoms; it += kIssuers) {
+        ok = ok && !*abort_flag && mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns) &&
+             mbar_wait(&full[slot], phase, a.err, a.wait_ns);
+        if (!ok) break;
+        fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
+        tc_fence_after();
+        const uint64_t ad = sw128_kmajor_desc(smem_u32(smem + L.ring + slot * kSlotBytes));
+        const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + i * L.q_atom));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss<true>(tmem + acc * acc_cols, sw128_kmajor_desc(ab + kk * 32), sw128_kmajor_desc(bb + kk * 32), idesc,
-                         kk != 0);
-          mma_commit(&empty[slot]);
-          mma_commit(&s_full[acc]);
-          if (++slot == a.slots) {
-            slot = 0;
-            phase ^= 1;
-          }
-          if (++acc == kAccs) {
-            acc = 0;
-            aphase ^= 1;
-          }
+        for (int kk = 0; kk < 4; ++kk)  // 32 bytes further in the 128-byte rows: 2 in address / 16
+          mma_ss<true>(tmem + acc * acc_cols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+        mma_commit(&empty[slot]);
+        mma_commit(&s_full[acc]);
+        i = i + kIssuers < kAtoms ? i + kIssuers : i + kIssuers - kAtoms;
+        slot += kIssuers;
+        if (slot >= a.slots) {
+          slot -= a.slots;
+          phase ^= 1;
+        }
+        acc += kIssuers;
+        if (acc >= kAccs) {
+          acc -= kAccs;
+          aphase ^= 1;
         }
       }
       if (!ok) *abort_flag = 1;
@@ -303,16 +389,24 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   } else if (warp < kSumWarps && nblk > 0) {
     // ---------------------------------------------------------------- sums
     const int wg = warp >> 2, r = threadIdx.x & 127;  // half of the heads, row of the block
-    const int heads = a.H >> 1, h0 = wg * heads;
+    const int heads = a.hg >> 1, h0 = wg * heads;
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h0;
-    const float inv_h = 1.f / (float)a.H;  // a power of two
-    float* other = reinterpret_cast<float*>(smem + L.half);
+    const float inv_h = 1.f / (float)a.H, most = (float)heads * inv_h;  // powers of two
     bool ok = __all_sync(0xffffffffu, mbar_wait(ready, 0, a.err, a.wait_ns));
+    if constexpr (kKv8) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err, a.wait_ns));
+      if (ok) query_to_f16(smem, L.q_atom, a.hg, a.c_hi, a.c_lo, head);
+      fence_proxy_async_smem();  // the MMAs read the query through the async proxy
+      sums_sync();               // the factors that other threads wrote
+      if (lane == 0) mbar_arrive(q_half);
+    }
     int acc = 0, aphase = 0;
     for (int j = 0; j < nblk; ++j) {
       const int k = j * kRows + r;
       const bool live = ok && rows[k] >= 0;
       const int s = live ? __ldg(a.idx + (int64_t)t * a.K + kbeg + k) : 0;
+      uint2 tiles = make_uint2(0u, 0u);  // FP8 cache: the row's tile scales
+      if constexpr (kKv8) tiles = live ? ld_nc_v2(a.kv_scale + (int64_t)rows[k] * 8) : tiles;
       float x[CH][32];
 #pragma unroll
       for (int i = 0; i < kAtoms; ++i) {
@@ -323,11 +417,18 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
 #pragma unroll
           for (int c = 0; c < CH; ++c) tmem_ld32(t_lane + acc * acc_cols + 32 * c, v[c]);
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            tmem_ld_wait_regs(v[c]);
+          for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(v[c]);
+          const float sc = kKv8 ? tile_scale((i < 8 ? tiles.x >> (8 * (i >> 1)) : tiles.y) & 0xFFu) : 1.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[c][e] = i == 0 ? __uint_as_float(v[c][e]) : x[c][e] + __uint_as_float(v[c][e]);
-          }
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __uint_as_float(v[c][e]);
+              if constexpr (kKv8)
+                x[c][e] = i == 0 ? y * sc : fmaf(y, sc, x[c][e]);
+              else
+                x[c][e] = i == 0 ? y : x[c][e] + y;
+            }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[acc]);
@@ -342,22 +443,14 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 lh = lse[h0 + 32 * c + e];
-          const float p = ex2_ftz(fmaf(x[c][e], a.c_hi, -lh.x) + fmaf(x[c][e], a.c_lo, -lh.y));
+          const float4 h = head[h0 + 32 * c + e];
+          const float p = ex2_ftz(fmaf(x[c][e], h.z, -h.x) + fmaf(x[c][e], h.w, -h.y));
           if (32 * c + e < heads) sum[e & 3] += p;
         }
-      float w = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      // the second half's sum goes through shared memory, two buffers: the ring of
-      // accumulators lets no warp run a whole block ahead of another
-      if (wg == 1) {
-        other[(j & 1) * kRows + r] = w;
-        sums_arrive();
-        continue;
-      }
-      sums_wait();
-      w = (w + other[(j & 1) * kRows + r]) * inv_h;
+      // this half's share of the mean over all heads
+      const float w = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * inv_h;
       // a NaN (from a NaN or an lse that does not belong to these logits) adds nothing
-      const float lim = w > 0.f ? fminf(w, 1.f) : 0.f;
+      const float lim = w > 0.f ? fminf(w, most) : 0.f;
       if (ok && live && lim > 0.f)
         atomicAdd(a.mass + (int64_t)at.seq * a.ld + s, (unsigned long long)__float2ll_rn(lim * 0x1p40f));
     }
@@ -392,17 +485,27 @@ int mass_splits(int T, int K) {
 }
 
 template <bool kKv8, int CH>
-cudaError_t launch(const CUtensorMap& tq, const MassArgs& a, int64_t ctas, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& tq, MassArgs a, cudaStream_t st) {
+  using R = Roles<kKv8, CH>;
   static thread_local int attr_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (attr_dev != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_mass<kKv8, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    cudaError_t e =
+        cudaFuncSetAttribute(k_attn_mass<kKv8, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     attr_dev = dev;
   }
-  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(kThreads),
-                    (size_t)(Layout(a.H, a.slots).total + 1024), st, tq, a);
+  a.hg = kKv8 && a.H > 64 ? 64 : a.H;
+  const int T = a.s.num_tokens * (a.H / a.hg), blocks = (a.K + kRows - 1) / kRows;
+  const int sp = mass_splits(T, a.K), per = (blocks + sp - 1) / sp;
+  a.ks = per * kRows;
+  a.splits = (blocks + per - 1) / per;
+  a.slots = R::slots;
+  const int64_t ctas = (int64_t)T * a.splits;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(R::threads),
+                    (size_t)(Layout(a.hg, a.slots, R::ahead * R::groups, a.ks).total + 1024), st, tq, a);
 }
 
 }  // namespace
@@ -411,18 +514,13 @@ cudaError_t launch_attn_mass(const SeqsDev& s, const __nv_bfloat16* q, const voi
                              const int32_t* idx, int K, int H, float scale, const float* lse, int64_t* mass,
                              int64_t ld, uint32_t* err, cudaStream_t st) {
   CUtensorMap tq;
-  if (!make_bf16_rows_map(&tq, q, kDQK, (uint64_t)s.num_tokens * H, H)) return cudaErrorInvalidValue;
-  const int blocks = (K + kRows - 1) / kRows;
-  const int per = (blocks + mass_splits(s.num_tokens, K) - 1) / mass_splits(s.num_tokens, K);
-  const int splits = (blocks + per - 1) / per;
+  if (!make_bf16_rows_map(&tq, q, kDQK, (uint64_t)s.num_tokens * H, kv8_scale && H > 64 ? 64 : H)) return cudaErrorInvalidValue;
   const double c = (double)scale * 1.4426950408889634;
   const float c_hi = (float)c;
-  MassArgs a{s,  static_cast<const uint8_t*>(kv), kv8_scale, idx, lse, reinterpret_cast<unsigned long long*>(mass),
-             ld, K, H, per * kRows, splits, H == 128 ? 4 : kMaxSlots, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
-  const int64_t ctas = (int64_t)s.num_tokens * splits;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaError_t e = H == 128 ? (kv8_scale ? launch<true, 2>(tq, a, ctas, st) : launch<false, 2>(tq, a, ctas, st))
-                           : (kv8_scale ? launch<true, 1>(tq, a, ctas, st) : launch<false, 1>(tq, a, ctas, st));
+  const MassArgs a{s, static_cast<const uint8_t*>(kv), kv8_scale, idx, lse, reinterpret_cast<unsigned long long*>(mass),
+                   ld, K, H, 0, 0, 0, 0, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
+  cudaError_t e = kv8_scale ? launch<true, 1>(tq, a, st)
+                            : (H == 128 ? launch<false, 2>(tq, a, st) : launch<false, 1>(tq, a, st));
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }

@@ -149,6 +149,28 @@ def test_mass_one_position_from_many_tokens(lib):
     assert ((got - q_len).abs() <= 2e-3 * q_len).all()
 
 
+@pytest.mark.parametrize("kv_fp8", [False, True])
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_mass_many_blocks_and_waves(lib, heads, kv_fp8):
+    """Full lists for more tokens than SMs, again and again: every wait ends, and
+    every run adds the same integers."""
+    wl = make_workload(SMALL["chunked_small"].scaled(name=f"waves_{heads}_{kv_fp8}", heads=heads, kv_fp8=kv_fp8,
+                                                     batch=2, prefix=(2100, 2200), chunk=(190, 200), topk=2048))
+    d = to_device(wl)
+    idx = torch.from_numpy(np.tile(np.arange(2048, dtype=np.int32), (wl.T, 1))).cuda()
+    _, lse = lib.dsa_sparse_mla_fwd(d.seqs, d.q, d.kv, idx, wl.scale, kv_scale=d.kv_scale)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(40):
+        mass = torch.zeros((2, wl.max_ctx), dtype=torch.int64, device="cuda")
+        lib.dsa_attn_mass(d.seqs, d.q, d.kv, idx, lse, wl.scale, mass, kv_scale=d.kv_scale, ws=ws)
+        first = mass if first is None else first
+        assert torch.equal(mass, first)
+    assert lib.dsa_check_error(ws) == lib.DSA_OK
+    q_len = torch.from_numpy(np.diff(wl.q_seq_start)).double()
+    assert ((first.sum(1).cpu().double() * UNIT - q_len).abs() <= 2e-3 * q_len).all()
+
+
 # ---------------------------------------------------------------------------
 
 
