@@ -12,19 +12,18 @@
 // inside one thread -- the transposed product of the attention kernel would
 // need a reduction over lanes -- and a row is gathered once for all heads.
 //   * four loader warps resolve the slice's rows (index list -> page table ->
-//     pool row) and copy them, 128 rows x 64 dims (16 KB) at a time, into a ring of
-//     128-byte-swizzled operand slots, each with its own barriers: the query
-//     (H x 1152 bytes) fills most of shared memory, and the ring keeps loads in
-//     flight across blocks;
-//   * three threads, each taking every third slot, issue the MMAs, four per
-//     slot, each slot's 64 dims into an accumulator of its own (a ring of four): one
-//     thread's waits, fence, issue and commits of a slot are a serial 900 cycles, three
-//     times what the slot's rows take to arrive;
+//     pool row) and copy them, 128 rows x 128 dims (a tile, 32 KB; the last of a
+//     row's five is half of one) at a time, into a ring of 128-byte-swizzled operand
+//     slots, each with its own barriers: the query (H x 1152 bytes) fills most of
+//     shared memory, and the ring keeps loads in flight across blocks;
+//   * two threads, taking tiles in turn, issue the MMAs, eight per tile, each
+//     tile into an accumulator of its own (a ring of four): the waits, fence, issue and
+//     commits are one serial chain per tile, and two of them overlap;
 //   * eight warps, two per lane quarter with half of the heads each, add the
-//     nine partial logits in registers and take p = 2^(c S - L_h), summed over h.
+//     five partial logits in registers and take p = 2^(c S - L_h), summed over h.
 // FP8 cache.  Its codes become fp16, one conversion instruction per pair and exact;
 // their tiles' scales, powers of two per row, multiply the partial logits instead
-// (a tile is two slots), in the thread that owns the row.  The query becomes fp16 as
+// in the thread that owns the row.  The query becomes fp16 as
 // well, each head times the power of two that brings its largest value to 2^14:
 // values 2^-28 of that and less lose bits, 2^-39 of the largest at most.  (As bf16
 // the codes cost five times the instructions, and that bounded the kernel: 106 us
@@ -32,7 +31,7 @@
 // memory for the staged codes and registers for twice the loader warps.
 // Precision.  The tensor core's fp32 additions truncate: one chain of 36
 // accumulations per logit was off by 3e-6 of the mass (an fp32 product rounded to
-// nearest: 6.5e-7), all one way.  Chains of four, added with rounding, are not.
+// nearest: 6.5e-7), all one way.  Chains of eight, added with rounding, are not.
 // c = scale log2 e and L = lse log2 e are used as two fp32 terms each: one would
 // be off by 2^-24 of the logit, 1e-6 of p at logits of 16.
 //
@@ -53,16 +52,17 @@ using namespace sm100;
 
 constexpr int kRows = 128;                   // rows per block (the MMA's M)
 constexpr int kAtoms = kDQK / 64;            // 9 slices of 64 dims
-constexpr int kSlotBytes = kRows * 128;
+constexpr int kAtomBytes = kRows * 128;
+constexpr int kTiles = 5;                    // of a row: two atoms each, the last one
+constexpr int kSlotBytes = 2 * kAtomBytes;
 constexpr int kSumWarps = 8;                 // warps 0-7
-constexpr int kIssuers = 3;                  // warps 8-10, one thread each; warp 8 owns TMEM
+constexpr int kIssuers = 2;                  // warps 8-9, one thread each; warp 8 owns TMEM
 constexpr int kLoaderBarrier = 1, kSumBarrier = 2;
 constexpr int kMmaWarp = kSumWarps;
 constexpr int kLoadWarp = kMmaWarp + kIssuers;
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 4;
 constexpr int kAccs = 4;                     // accumulators of up to 128 columns
 constexpr int kTmemCols = 512;
-static_assert(kAtoms % kIssuers == 0, "each issuer takes the same atoms of every block");
 
 struct MassArgs {
   SeqsDev s;
@@ -133,21 +133,19 @@ __device__ __forceinline__ void query_to_f16(uint8_t* q, int q_atom, int heads, 
   }
 }
 
-// Operand slots and staged FP8 codes (8 KB per atom) share what the query leaves.
+// Operand slots and staged FP8 codes (16 KB per tile) share what the query leaves.
 template <bool kKv8, int CH>
 struct Roles {
   static_assert(!kKv8 || CH == 1, "FP8 cache: up to 64 heads per CTA");
-  static constexpr int groups = kKv8 ? kIssuers : 1;  // loader groups, taking atoms in turn
-  static constexpr int loaders = kKv8 ? 64 * groups : 128;
+  static constexpr int groups = kKv8 ? 2 : 1;    // loader groups of 128 threads, taking tiles in turn
+  static constexpr int loaders = 128 * groups;
   static constexpr int threads = 32 * kLoadWarp + loaders;
   // A barrier's parity tells its next phase from this one, not from the one after, so
-  // nobody may wait for a slot two uses ahead.  A loader waits for its slot's release in
-  // the order of uses: alone, or (groups) because a slot always comes back to the same
-  // group.  An issuer waits for its accumulator first, whose release says that every
-  // atom up to the fourth before was summed, so the slot's earlier use is over.
-  static constexpr int slots = kKv8 ? 6 : (CH == 2 ? 4 : 8);
-  static_assert(slots % groups == 0 && slots >= kAccs && slots <= kMaxSlots && kAccs > kIssuers, "see above");
-  static constexpr int ahead = kKv8 ? 2 : 0;     // atoms that a group stages ahead
+  // nobody may wait for a slot or an accumulator two uses ahead: each comes back to
+  // the same issuer and the same loader group, which waits in the order of its uses.
+  static constexpr int slots = kKv8 || CH == 2 ? 2 : 4;
+  static_assert(slots % groups == 0 && slots % kIssuers == 0 && kAccs % kIssuers == 0, "see above");
+  static constexpr int ahead = kKv8 ? 2 : 0;     // tiles that a group stages ahead
 };
 
 // CH: chunks of 32 heads that a summing thread holds (two for H = 128).
@@ -266,16 +264,18 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) row[u] = rows[j * kRows + rsub + kStep * u];
 #pragma unroll
-        for (int i = 0; i < kAtoms; ++i) {
+        for (int i = 0; i < kTiles; ++i) {
           ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
           if (ok) {
             const uint32_t dst = ring + slot * kSlotBytes + swz;
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-              const bool live = row[u] >= 0;
-              const uint8_t* src = a.kv + (live ? (int64_t)row[u] * (kDQK * 2) : 0) + 128 * i + 16 * piece;
-              cp_async_16_zfill(dst + u * kStep * 128, src, live ? 16u : 0u);
-            }
+            for (int h = 0; h < (i < kTiles - 1 ? 2 : 1); ++h)
+#pragma unroll
+              for (int u = 0; u < kUnits; ++u) {
+                const bool live = row[u] >= 0;
+                const uint8_t* src = a.kv + (live ? (int64_t)row[u] * (kDQK * 2) : 0) + 256 * i + 128 * h + 16 * piece;
+                cp_async_16_zfill(dst + h * kAtomBytes + u * kStep * 128, src, live ? 16u : 0u);
+              }
             cp_async_mbar_arrive(&full[slot]);  // counts once this thread's copies land
           }
           if (++slot == a.slots) {
@@ -285,55 +285,66 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
         }
       }
     } else {
-      // Group g of 64 threads takes atoms g, g + 3, ...: the waits, fence and barrier of
-      // an atom cost each warp as much as its conversions.  Thread: rows rsub + 16 u, 16
-      // codes each.  They come kAhead of the group's atoms early into a place of the
+      // Group g of 128 threads takes tiles g, g + 2, ...: the waits, fence and barrier
+      // of a tile cost each warp as much as its conversions.  Thread: rows rsub + 16 u, 16
+      // codes each.  They come kAhead of the group's tiles early into a place of the
       // thread's own (no barrier), are converted and stored where the bf16 gather
       // would have put the values.  A row that is not live reads row 0 of the pool:
       // its logits, in a lane of their own, are not used.
       using R = Roles<kKv8, CH>;
-      constexpr int kGroup = kLoaders / R::groups, kUnits = kRows * 4 / kGroup, kAhead = R::ahead;
-      static_assert(kGroup == 64 && kUnits == 8, "16 rows per step");
-      const int g = li / kGroup, lt = li % kGroup, rsub = lt >> 2, piece = lt & 3;
+      constexpr int kGroup = kLoaders / R::groups, kUnits = kRows * 8 / kGroup, kAhead = R::ahead;
+      static_assert(kGroup == 128 && kUnits == 8, "16 rows per step");
+      const int g = li / kGroup, lt = li % kGroup, rsub = lt >> 3, piece = lt & 7;
       uint8_t* stage = smem + L.stage + g * (kAhead * kSlotBytes / 2) + lt * 16;
-      const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)(2 * piece) ^ ((uint32_t)rsub & 7u)) << 4);
-      const int total = nblk * kAtoms;
-      int next = g, next_place = 0;  // the next atom to fetch and its place
+      // 16 codes fill two 16-byte pieces; the second atom's lanes write theirs in
+      // the other order, so that a row's eight lanes hit eight different bank groups
+      const uint32_t base = (uint32_t)(piece >> 2) * kAtomBytes + (uint32_t)rsub * 128u;
+      const uint32_t swz = base + (((uint32_t)(2 * (piece & 3) + (piece >> 2)) ^ ((uint32_t)rsub & 7u)) << 4);
+      const bool second = piece >= 4;
+      const int total = nblk * kTiles;
+      int next = g, next_place = 0;  // the next tile to fetch and its place
       auto fetch = [&]() {
         if (next < total) {
-          const int j = next / kAtoms, i = next - j * kAtoms;
-          const uint8_t* src = a.kv + 64 * i + 16 * piece;
-          const int32_t* rj = rows + j * kRows + rsub;
+          const int j = next / kTiles, i = next - j * kTiles;
+          if (i < kTiles - 1 || !second) {
+            const uint8_t* src = a.kv + 128 * i + 16 * piece;
+            const int32_t* rj = rows + j * kRows + rsub;
 #pragma unroll
-          for (int u = 0; u < kUnits; ++u)
-            cp_async_16(stage + (next_place * kUnits + u) * (kGroup * 16), src + (int64_t)max(rj[16 * u], 0) * kDQK);
+            for (int u = 0; u < kUnits; ++u)
+              cp_async_16(stage + (next_place * kUnits + u) * (kGroup * 16), src + (int64_t)max(rj[16 * u], 0) * kDQK);
+          }
           next += R::groups;
           if (++next_place == kAhead) next_place = 0;
         }
         cp_async_commit();
       };
       for (int i = 0; i < kAhead; ++i) fetch();
-      int place = 0;
-      slot = g;  // a.slots exceeds the groups
+      int place = 0, tile = g;
+      slot = g;
       for (int it = g; it < total; it += R::groups) {
-        cp_async_wait<kAhead - 1>();  // this thread's codes of the atom are in place
+        cp_async_wait<kAhead - 1>();  // this thread's codes of the tile are in place
         uint4 c[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
           c[u] = *reinterpret_cast<const uint4*>(stage + (place * kUnits + u) * (kGroup * 16));
         if (++place == kAhead) place = 0;
+        fetch();
         ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns));
         if (!ok) break;
-        uint8_t* dst = smem + L.ring + slot * kSlotBytes;
+        if (tile < kTiles - 1 || !second) {
+          uint8_t* dst = smem + L.ring + slot * kSlotBytes;
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          *reinterpret_cast<uint4*>(dst + swz + u * 2048) = e4m3x8_to_f16x8(make_uint2(c[u].x, c[u].y));
-          *reinterpret_cast<uint4*>(dst + (swz ^ 16u) + u * 2048) = e4m3x8_to_f16x8(make_uint2(c[u].z, c[u].w));
+          for (int u = 0; u < kUnits; ++u) {
+            const uint4 lo = e4m3x8_to_f16x8(make_uint2(c[u].x, c[u].y));
+            const uint4 hi = e4m3x8_to_f16x8(make_uint2(c[u].z, c[u].w));
+            *reinterpret_cast<uint4*>(dst + swz + u * 2048) = second ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + (swz ^ 16u) + u * 2048) = second ? lo : hi;
+          }
         }
         fence_proxy_async_smem();  // the MMAs read these stores through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[slot]);
-        fetch();
+        tile = tile + R::groups < kTiles ? tile + R::groups : tile + R::groups - kTiles;
         slot += R::groups;
         if (slot >= a.slots) {
           slot -= a.slots;
@@ -350,23 +361,27 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       const uint32_t idesc = make_idesc(!kKv8, kRows, a.hg);  // bf16 or (FP8 cache) fp16 operands
       bool ok = mbar_wait(kKv8 ? q_half : q_full, 0, a.err, a.wait_ns);
       if constexpr (kKv8) fence_proxy_async_smem();  // the query was rewritten by the summing warps
-      int i = warp - kMmaWarp;  // atom of the block
-      int slot = i, phase = 0;  // a.slots and kAccs exceed kIssuers
-      int acc = i, aphase = 0;
-      for (int it = i; it < nblk * kAtoms; it += kIssuers) {
+      int i = warp - kMmaWarp;  // tile of the block
+      int slot = i, phase = 0, acc = i, aphase = 0;
+      for (int it = i; it < nblk * kTiles; it += kIssuers) {
         ok = ok && !*abort_flag && mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns) &&
              mbar_wait(&full[slot], phase, a.err, a.wait_ns);
         if (!ok) break;
         fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
         tc_fence_after();
         const uint64_t ad = sw128_kmajor_desc(smem_u32(smem + L.ring + slot * kSlotBytes));
-        const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + i * L.q_atom));
+        const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + 2 * i * L.q_atom));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 bytes further in the 128-byte rows: 2 in address / 16
-          mma_ss<true>(tmem + acc * acc_cols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+        for (int h = 0; h < 2; ++h) {  // descriptors move by bytes / 16: an atom, or 32 bytes in the 128-byte rows
+          if (h == 1 && i == kTiles - 1) break;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss<true>(tmem + acc * acc_cols, ad + h * (kAtomBytes / 16) + 2 * kk, bd + h * (L.q_atom / 16) + 2 * kk,
+                         idesc, (h | kk) != 0);
+        }
         mma_commit(&empty[slot]);
         mma_commit(&s_full[acc]);
-        i = i + kIssuers < kAtoms ? i + kIssuers : i + kIssuers - kAtoms;
+        i = i + kIssuers < kTiles ? i + kIssuers : i + kIssuers - kTiles;
         slot += kIssuers;
         if (slot >= a.slots) {
           slot -= a.slots;
@@ -409,7 +424,7 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       if constexpr (kKv8) tiles = live ? ld_nc_v2(a.kv_scale + (int64_t)rows[k] * 8) : tiles;
       float x[CH][32];
 #pragma unroll
-      for (int i = 0; i < kAtoms; ++i) {
+      for (int i = 0; i < kTiles; ++i) {
         ok = ok && __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[acc], aphase, a.err, a.wait_ns));
         if (ok) {
           tc_fence_after();
@@ -418,7 +433,7 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
           for (int c = 0; c < CH; ++c) tmem_ld32(t_lane + acc * acc_cols + 32 * c, v[c]);
 #pragma unroll
           for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(v[c]);
-          const float sc = kKv8 ? tile_scale((i < 8 ? tiles.x >> (8 * (i >> 1)) : tiles.y) & 0xFFu) : 1.f;
+          const float sc = kKv8 ? tile_scale((i < kTiles - 1 ? tiles.x >> (8 * i) : tiles.y) & 0xFFu) : 1.f;
 #pragma unroll
           for (int c = 0; c < CH; ++c)
 #pragma unroll
