@@ -21,14 +21,14 @@
 //     commits are one serial chain per tile, and two of them overlap;
 //   * eight warps, two per lane quarter with half of the heads each, add the
 //     five partial logits in registers and take p = 2^(c S - L_h), summed over h.
-// FP8 cache.  Its codes become fp16, one conversion instruction per pair and exact;
-// their tiles' scales, powers of two per row, multiply the partial logits instead
-// in the thread that owns the row.  The query becomes fp16 as
-// well, each head times the power of two that brings its largest value to 2^14:
-// values 2^-28 of that and less lose bits, 2^-39 of the largest at most.  (As bf16
-// the codes cost five times the instructions, and that bounded the kernel: 106 us
-// where the bf16 cache takes 47.)  A CTA takes 64 heads then, which leaves shared
-// memory for the staged codes and registers for twice the loader warps.
+// FP8 cache.  The tensor core multiplies its E4M3 codes as they are.  The tiles'
+// scales, a power of two per row and tile, multiply the partial logits in the thread
+// that owns the row.  The query becomes two E4M3 terms, q 2^s = t1 + 2^-5 t2 with the
+// head's largest value in [2^7, 2^8): a bf16 has eight significant bits and each term
+// holds four, so their sum is exact down to 2^-14 of that value and off by 2^-22 of it
+// at most below.  They are 2 H columns of one product of twice the rate.
+// (Converting the codes instead, to bf16 or fp16 for one product, took 2.7 and 1.6
+// times as long: a tile then crosses shared memory four times.)
 // Precision.  The tensor core's fp32 additions truncate: one chain of 36
 // accumulations per logit was off by 3e-6 of the mass (an fp32 product rounded to
 // nearest: 6.5e-7), all one way.  Chains of eight, added with rounding, are not.
@@ -54,41 +54,39 @@ constexpr int kRows = 128;                   // rows per block (the MMA's M)
 constexpr int kAtoms = kDQK / 64;            // 9 slices of 64 dims
 constexpr int kAtomBytes = kRows * 128;
 constexpr int kTiles = 5;                    // of a row: two atoms each, the last one
-constexpr int kSlotBytes = 2 * kAtomBytes;
 constexpr int kSumWarps = 8;                 // warps 0-7
 constexpr int kIssuers = 2;                  // warps 8-9, one thread each; warp 8 owns TMEM
 constexpr int kLoaderBarrier = 1, kSumBarrier = 2;
 constexpr int kMmaWarp = kSumWarps;
 constexpr int kLoadWarp = kMmaWarp + kIssuers;
-constexpr int kMaxSlots = 4;
-constexpr int kAccs = 4;                     // accumulators of up to 128 columns
+constexpr int kMaxSlots = 8;
+constexpr int kMaxAccs = 4;
 constexpr int kTmemCols = 512;
 
 struct MassArgs {
   SeqsDev s;
+  const __nv_bfloat16* q;
   const uint8_t* kv;         // bf16 rows, or E4M3 codes
   const uint8_t* kv_scale;   // FP8 cache: tile-scale bytes [rows, 8]
   const int32_t* idx;
   const float* lse;
   unsigned long long* mass;
   int64_t ld;
-  int K, H, hg, ks, splits, slots;  // hg heads per CTA
+  int K, H, ks, splits;
   float c_hi, c_lo;          // scale * log2(e) as two terms
   uint32_t* err;
   uint64_t wait_ns;
 };
 
-// Shared memory from a 1024-aligned base: query, ring, staged codes, rows, lse, barriers.
+// Shared memory from a 1024-aligned base: query, ring, rows, heads, barriers.
 struct Layout {
-  int q_atom, ring, stage, rows, head, bars, total;
-  __host__ __device__ Layout(int H, int slots, int ahead, int ks) {
-    q_atom = H * 128;
-    ring = kAtoms * q_atom;
-    stage = ring + slots * kSlotBytes;
-    rows = stage + ahead * (kSlotBytes / 2);
+  int ring, rows, head, bars, total;
+  __host__ __device__ Layout(int H, int ring_bytes, int ks) {
+    ring = kAtoms * H * 128;
+    rows = ring + ring_bytes;
     head = rows + ks * 4;                  // and 32 entries more: chunks of 32 heads are read whole
     bars = head + H * 16 + 512;
-    total = bars + (2 * kMaxSlots + 2 * kAccs + 5) * 8 + 16;
+    total = bars + (2 * kMaxSlots + 2 * kMaxAccs + 5) * 8 + 16;
   }
 };
 
@@ -97,95 +95,115 @@ __device__ __forceinline__ void sums_sync() {
   asm volatile("barrier.cta.sync %0, %1;" ::"n"(kSumBarrier), "n"(kSumWarps * 32) : "memory");
 }
 
-// FP8 cache: the query tile in shared memory from bf16 to fp16, in place, by the
-// summing warps.  256 / heads neighbouring threads share a head; its factor becomes
-// scale log2(e) / 2^s with s the power that was multiplied in.
-__device__ __forceinline__ void query_to_f16(uint8_t* q, int q_atom, int heads, float c_hi, float c_lo, float4* head) {
-  const int per = kSumWarps * 32 / heads;        // threads per head: 4, 8 or 16
+// FP8 cache: the token's query as two E4M3 terms in shared memory, by the summing
+// warps.  Tile i of the operand holds 2 H rows (the heads' first terms, then their
+// second ones) of 128 dims in the 128-byte swizzle, the last tile 64 dims in the
+// 64-byte swizzle.  256 / H neighbouring threads share a head; its factor becomes
+// scale log2(e) / 2^s.  (Two passes over the query, the second from L2: 128 heads
+// would not fit in registers.)
+__device__ __forceinline__ void query_to_e4m3(const __nv_bfloat16* q, uint8_t* dst, int H, float c_hi, float c_lo,
+                                              float4* head) {
+  const int per = kSumWarps * 32 / H;            // threads per head: 2, 4, 8 or 16
   const int h = threadIdx.x / per, sub = threadIdx.x % per;
-  const int chunks = kAtoms * 8;                 // 16-byte pieces of a head
+  constexpr int kChunks = kDQK / 8;              // 16-byte pieces of a head
+  const uint4* src = reinterpret_cast<const uint4*>(q + (int64_t)h * kDQK);
   uint32_t m = 0;
-  for (int k = sub; k < chunks; k += per) {
-    const uint4 v = *reinterpret_cast<const uint4*>(q + (k >> 3) * q_atom + h * 128 + (k & 7) * 16);
+#pragma unroll 18
+  for (int k = sub; k < kChunks; k += per) {
+    const uint4 v = __ldg(src + k);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
   }
   for (int o = 1; o < per; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // largest value to [2^14, 2^15); zero, infinite and NaN heads keep their scale
-  int s = m == 0u || m >= 0x7F80u ? 0 : 141 - (int)(m >> 7);
-  s = min(s, 126);
+  // largest value to [2^7, 2^8); a head with an infinity or NaN, which the terms
+  // would lose, gets a factor of NaN
+  const int s = min(126, m == 0u || m >= 0x7F80u ? 0 : 134 - (int)(m >> 7));
   const float up = __uint_as_float((uint32_t)(127 + s) << 23), down = __uint_as_float((uint32_t)(127 - s) << 23);
-  for (int k = sub; k < chunks; k += per) {
-    uint4* at = reinterpret_cast<uint4*>(q + (k >> 3) * q_atom + h * 128 + (k & 7) * 16);
-    uint4 v = *at;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 9
+  for (int k = sub; k < kChunks; k += per) {
+    const uint4 v = __ldg(src + k);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t t1[2] = {0u, 0u}, t2[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 r = __floats2half2_rn(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-      w[i] = *reinterpret_cast<const uint32_t*>(&r);
+      const float2 f = make_float2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+      const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+      const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+      const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&ar));
+      const __nv_fp8x2_storage_t b =
+          __nv_cvt_float2_to_fp8x2(make_float2((f.x - g.x) * 32.f, (f.y - g.y) * 32.f), __NV_SATFINITE, __NV_E4M3);
+      t1[i >> 1] |= (uint32_t)a << (16 * (i & 1));
+      t2[i >> 1] |= (uint32_t)b << (16 * (i & 1));
     }
-    *at = make_uint4(w[0], w[1], w[2], w[3]);
+    const int tile = k >> 4, piece = (k & 15) >> 1;  // 16-byte piece of the row, this thread's half of it
+    uint8_t* at = dst + tile * (2 * H * 128) + 8 * (k & 1);
+    int second;
+    if (tile < kTiles - 1) {
+      at += h * 128 + ((piece ^ (h & 7)) << 4);
+      second = H * 128;
+    } else {
+      at += h * 64 + ((piece ^ ((h >> 1) & 3)) << 4);
+      second = H * 64;
+    }
+    *reinterpret_cast<uint2*>(at) = make_uint2(t1[0], t1[1]);
+    *reinterpret_cast<uint2*>(at + second) = make_uint2(t2[0], t2[1]);  // H is a multiple of 16: the same swizzle
   }
   if (sub == 0) {
-    head[h].z = c_hi * down;
+    head[h].z = m < 0x7F80u ? c_hi * down : __uint_as_float(0x7FC00000u);
     head[h].w = c_lo * down;
   }
 }
 
-// Operand slots and staged FP8 codes (16 KB per tile) share what the query leaves.
+constexpr int kLoaders = 128;
+constexpr int kThreads = 32 * kLoadWarp + kLoaders;
+constexpr int kPerLoader = kMaxK / kLoaders;  // list entries a loader resolves
+
+// A barrier's parity tells its next phase from this one, not from the one after, so
+// nobody may wait for a slot or an accumulator two uses ahead: the one loader group
+// waits in order, and each slot and accumulator comes back to the same issuer.
 template <bool kKv8, int CH>
-struct Roles {
-  static_assert(!kKv8 || CH == 1, "FP8 cache: up to 64 heads per CTA");
-  static constexpr int groups = kKv8 ? 2 : 1;    // loader groups of 128 threads, taking tiles in turn
-  static constexpr int loaders = 128 * groups;
-  static constexpr int threads = 32 * kLoadWarp + loaders;
-  // A barrier's parity tells its next phase from this one, not from the one after, so
-  // nobody may wait for a slot or an accumulator two uses ahead: each comes back to
-  // the same issuer and the same loader group, which waits in the order of its uses.
-  static constexpr int slots = kKv8 || CH == 2 ? 2 : 4;
-  static_assert(slots % groups == 0 && slots % kIssuers == 0 && kAccs % kIssuers == 0, "see above");
-  static constexpr int ahead = kKv8 ? 2 : 0;     // tiles that a group stages ahead
+struct Ring {
+  static constexpr int slot_bytes = (kKv8 ? 1 : 2) * kAtomBytes;  // 128 dims of 128 rows
+  static constexpr int slots = (CH == 2 ? 2 : 4) * (kKv8 ? 2 : 1);
+  static constexpr int accs = kKv8 && CH == 2 ? 2 : 4;            // of 2 H (FP8) or H columns
+  static_assert(slots % kIssuers == 0 && accs % kIssuers == 0 && slots <= kMaxSlots && accs <= kMaxAccs, "see above");
 };
 
 // CH: chunks of 32 heads that a summing thread holds (two for H = 128).
 template <bool kKv8, int CH>
-__global__ void __launch_bounds__(Roles<kKv8, CH>::threads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
-  constexpr int kLoaders = Roles<kKv8, CH>::loaders;
-  constexpr int kPerLoader = (kMaxK + kLoaders - 1) / kLoaders;  // list entries a loader resolves
+  using R = Ring<kKv8, CH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const Layout L(a.hg, a.slots, Roles<kKv8, CH>::ahead * Roles<kKv8, CH>::groups, a.ks);
+  const Layout L(a.H, R::slots * R::slot_bytes, a.ks);
   int32_t* rows = reinterpret_cast<int32_t*>(smem + L.rows);       // pool row of each slot of the slice, -1 = none
   float4* head = reinterpret_cast<float4*>(smem + L.head);          // per head: lse * log2(e), the logit's factor; two terms each
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* full = bars;                       // [slots]
   uint64_t* empty = bars + kMaxSlots;          // [slots]
-  uint64_t* s_full = bars + 2 * kMaxSlots;     // [kAccs]
-  uint64_t* s_empty = s_full + kAccs;          // [kAccs]
-  uint64_t* q_full = s_empty + kAccs;
-  uint64_t* q_half = q_full + 1;               // FP8 cache: the query is fp16
-  uint64_t* ready = q_half + 1;                // rows and lse are in shared memory
+  uint64_t* s_full = bars + 2 * kMaxSlots;     // [accs]
+  uint64_t* s_empty = s_full + kMaxAccs;       // [accs]
+  uint64_t* q_full = s_empty + kMaxAccs;       // the query's tile has landed, or (FP8 cache) its terms are written
+  uint64_t* ready = q_full + 1;                // rows and lse are in shared memory
   uint64_t* mma_drain = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = a.H / a.hg, unit = blockIdx.x / groups, head0 = (blockIdx.x % groups) * a.hg;
-  const int t = unit / a.splits, sp = unit % a.splits;
+  const int t = blockIdx.x / a.splits, sp = blockIdx.x % a.splits;
   const int kbeg = sp * a.ks, kend = min(a.K, kbeg + a.ks);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < a.slots; ++i) {
-      mbar_init(&full[i], kKv8 ? kLoaders / 32 / Roles<kKv8, CH>::groups : kLoaders);
+    for (int i = 0; i < R::slots; ++i) {
+      mbar_init(&full[i], kLoaders);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kAccs; ++i) {
+    for (int i = 0; i < R::accs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kSumWarps);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_half, kSumWarps);
+    mbar_init(q_full, kKv8 ? kSumWarps : 1);
     mbar_init(ready, 1);
     mbar_init(mma_drain, kIssuers);
     *abort_flag = 0;
@@ -204,11 +222,11 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   const TokenPlace at = locate_token(a.s, t);
   if (at.pos < 0 && threadIdx.x == 0) raise_error(a.err, kErrBadIndex);
   const int nblk = at.pos >= 0 && kend > kbeg ? (kend - kbeg + kRows - 1) / kRows : 0;
-  const int acc_cols = a.hg < 64 ? 64 : a.hg;
+  const int cols = (kKv8 ? 2 : 1) * a.H, acc_cols = cols < 64 ? 64 : cols;
 
-  if (threadIdx.x == kMmaWarp * 32 && nblk > 0) {
-    mbar_arrive_expect_tx(q_full, (uint32_t)(kAtoms * L.q_atom));
-    for (int i = 0; i < kAtoms; ++i) tma_load_2d(smem + i * L.q_atom, &tq, q_full, 64 * i, t * a.H + head0);
+  if (!kKv8 && threadIdx.x == kMmaWarp * 32 && nblk > 0) {
+    mbar_arrive_expect_tx(q_full, (uint32_t)(kAtoms * a.H * 128));
+    for (int i = 0; i < kAtoms; ++i) tma_load_2d(smem + i * a.H * 128, &tq, q_full, 64 * i, t * a.H);
   }
   if (warp >= kLoadWarp && nblk > 0) {
     // ---------------------------------------------------------------- loaders
@@ -238,8 +256,8 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
           raise_error(a.err, kErrBadIndex);
         if (k < nblk * kRows) rows[k] = row;
       }
-      if (li < a.hg) {
-        const float v = __ldg(a.lse + (int64_t)t * a.H + head0 + li);
+      if (li < a.H) {
+        const float v = __ldg(a.lse + (int64_t)t * a.H + li);
         constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266175e-8f;
         const float hi = v * kLog2e;
         // an infinite lse keeps its sign; its low term would be NaN
@@ -254,100 +272,36 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
     if (li == 0) mbar_arrive(ready);
     const uint32_t ring = smem_u32(smem + L.ring);
     int slot = 0, phase = 0;
-    if constexpr (!kKv8) {
-      // thread: rows rsub + kStep u, their 16-byte piece of each atom
-      constexpr int kUnits = kRows * 8 / kLoaders, kStep = kLoaders / 8;
-      const int rsub = li >> 3, piece = li & 7;
-      const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)piece ^ ((uint32_t)rsub & 7u)) << 4);
-      for (int j = 0; j < nblk && ok; ++j) {
-        int row[kUnits];
+    // thread: rows rsub + 16 u, their 16-byte piece of each 128 bytes
+    constexpr int kUnits = kRows * 8 / kLoaders, kStep = kLoaders / 8, kRowBytes = kKv8 ? kDQK : 2 * kDQK;
+    const int rsub = li >> 3, piece = li & 7;
+    const uint32_t swz = (uint32_t)rsub * 128u + (((uint32_t)piece ^ ((uint32_t)rsub & 7u)) << 4);
+    for (int j = 0; j < nblk && ok; ++j) {
+      int row[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) row[u] = rows[j * kRows + rsub + kStep * u];
+      for (int u = 0; u < kUnits; ++u) row[u] = rows[j * kRows + rsub + kStep * u];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
-          if (ok) {
-            const uint32_t dst = ring + slot * kSlotBytes + swz;
+      for (int i = 0; i < kTiles; ++i) {
+        ok = ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns);
+        if (ok) {
+          const uint32_t dst = ring + slot * R::slot_bytes + swz;
+          // the last tile: one atom of bf16, or the first 64 bytes of codes
+          const int atoms = kKv8 || i == kTiles - 1 ? 1 : 2;
+          if (!kKv8 || i < kTiles - 1 || piece < 4) {
 #pragma unroll
-            for (int h = 0; h < (i < kTiles - 1 ? 2 : 1); ++h)
+            for (int h = 0; h < atoms; ++h)
 #pragma unroll
               for (int u = 0; u < kUnits; ++u) {
                 const bool live = row[u] >= 0;
-                const uint8_t* src = a.kv + (live ? (int64_t)row[u] * (kDQK * 2) : 0) + 256 * i + 128 * h + 16 * piece;
+                const uint8_t* src =
+                    a.kv + (live ? (int64_t)row[u] * kRowBytes : 0) + i * R::slot_bytes / kRows + 128 * h + 16 * piece;
                 cp_async_16_zfill(dst + h * kAtomBytes + u * kStep * 128, src, live ? 16u : 0u);
               }
-            cp_async_mbar_arrive(&full[slot]);  // counts once this thread's copies land
           }
-          if (++slot == a.slots) {
-            slot = 0;
-            phase ^= 1;
-          }
+          cp_async_mbar_arrive(&full[slot]);  // counts once this thread's copies land
         }
-      }
-    } else {
-      // Group g of 128 threads takes tiles g, g + 2, ...: the waits, fence and barrier
-      // of a tile cost each warp as much as its conversions.  Thread: rows rsub + 16 u, 16
-      // codes each.  They come kAhead of the group's tiles early into a place of the
-      // thread's own (no barrier), are converted and stored where the bf16 gather
-      // would have put the values.  A row that is not live reads row 0 of the pool:
-      // its logits, in a lane of their own, are not used.
-      using R = Roles<kKv8, CH>;
-      constexpr int kGroup = kLoaders / R::groups, kUnits = kRows * 8 / kGroup, kAhead = R::ahead;
-      static_assert(kGroup == 128 && kUnits == 8, "16 rows per step");
-      const int g = li / kGroup, lt = li % kGroup, rsub = lt >> 3, piece = lt & 7;
-      uint8_t* stage = smem + L.stage + g * (kAhead * kSlotBytes / 2) + lt * 16;
-      // 16 codes fill two 16-byte pieces; the second atom's lanes write theirs in
-      // the other order, so that a row's eight lanes hit eight different bank groups
-      const uint32_t base = (uint32_t)(piece >> 2) * kAtomBytes + (uint32_t)rsub * 128u;
-      const uint32_t swz = base + (((uint32_t)(2 * (piece & 3) + (piece >> 2)) ^ ((uint32_t)rsub & 7u)) << 4);
-      const bool second = piece >= 4;
-      const int total = nblk * kTiles;
-      int next = g, next_place = 0;  // the next tile to fetch and its place
-      auto fetch = [&]() {
-        if (next < total) {
-          const int j = next / kTiles, i = next - j * kTiles;
-          if (i < kTiles - 1 || !second) {
-            const uint8_t* src = a.kv + 128 * i + 16 * piece;
-            const int32_t* rj = rows + j * kRows + rsub;
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u)
-              cp_async_16(stage + (next_place * kUnits + u) * (kGroup * 16), src + (int64_t)max(rj[16 * u], 0) * kDQK);
-          }
-          next += R::groups;
-          if (++next_place == kAhead) next_place = 0;
-        }
-        cp_async_commit();
-      };
-      for (int i = 0; i < kAhead; ++i) fetch();
-      int place = 0, tile = g;
-      slot = g;
-      for (int it = g; it < total; it += R::groups) {
-        cp_async_wait<kAhead - 1>();  // this thread's codes of the tile are in place
-        uint4 c[kUnits];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          c[u] = *reinterpret_cast<const uint4*>(stage + (place * kUnits + u) * (kGroup * 16));
-        if (++place == kAhead) place = 0;
-        fetch();
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&empty[slot], phase ^ 1, a.err, a.wait_ns));
-        if (!ok) break;
-        if (tile < kTiles - 1 || !second) {
-          uint8_t* dst = smem + L.ring + slot * kSlotBytes;
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) {
-            const uint4 lo = e4m3x8_to_f16x8(make_uint2(c[u].x, c[u].y));
-            const uint4 hi = e4m3x8_to_f16x8(make_uint2(c[u].z, c[u].w));
-            *reinterpret_cast<uint4*>(dst + swz + u * 2048) = second ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + (swz ^ 16u) + u * 2048) = second ? lo : hi;
-          }
-        }
-        fence_proxy_async_smem();  // the MMAs read these stores through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
-        tile = tile + R::groups < kTiles ? tile + R::groups : tile + R::groups - kTiles;
-        slot += R::groups;
-        if (slot >= a.slots) {
-          slot -= a.slots;
+        if (++slot == R::slots) {
+          slot = 0;
           phase ^= 1;
         }
       }
@@ -358,9 +312,9 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   } else if (warp >= kMmaWarp && warp < kLoadWarp && nblk > 0) {
     // ---------------------------------------------------------------- MMA issuers
     if (lane == 0) {
-      const uint32_t idesc = make_idesc(!kKv8, kRows, a.hg);  // bf16 or (FP8 cache) fp16 operands
-      bool ok = mbar_wait(kKv8 ? q_half : q_full, 0, a.err, a.wait_ns);
-      if constexpr (kKv8) fence_proxy_async_smem();  // the query was rewritten by the summing warps
+      const uint32_t idesc = make_idesc(!kKv8, kRows, cols);  // bf16, or E4M3 (kind::f8f6f4)
+      bool ok = mbar_wait(q_full, 0, a.err, a.wait_ns);
+      if constexpr (kKv8) fence_proxy_async_smem();  // the terms were written by the summing warps
       int i = warp - kMmaWarp;  // tile of the block
       int slot = i, phase = 0, acc = i, aphase = 0;
       for (int it = i; it < nblk * kTiles; it += kIssuers) {
@@ -369,34 +323,42 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
         if (!ok) break;
         fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
         tc_fence_after();
-        const uint64_t ad = sw128_kmajor_desc(smem_u32(smem + L.ring + slot * kSlotBytes));
-        const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + 2 * i * L.q_atom));
+        // descriptors move by bytes / 16: 32 bytes inside the swizzled rows, or an atom
+        const uint64_t ad = sw128_kmajor_desc(smem_u32(smem + L.ring + slot * R::slot_bytes));
+        const bool last = i == kTiles - 1;
+        if constexpr (kKv8) {
+          const uint32_t at = smem_u32(smem + i * cols * 128);
+          const uint64_t bd = last ? sw64_kmajor_desc(at) : sw128_kmajor_desc(at);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // descriptors move by bytes / 16: an atom, or 32 bytes in the 128-byte rows
-          if (h == 1 && i == kTiles - 1) break;
+          for (int kk = 0; kk < 4; ++kk)  // 32 dims each
+            if (kk < 2 || !last)
+              mma_ss<false>(tmem + acc * acc_cols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+        } else {
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(smem + 2 * i * a.H * 128));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss<true>(tmem + acc * acc_cols, ad + h * (kAtomBytes / 16) + 2 * kk, bd + h * (L.q_atom / 16) + 2 * kk,
-                         idesc, (h | kk) != 0);
+          for (int kk = 0; kk < 8; ++kk)  // 16 dims each
+            if (kk < 4 || !last)
+              mma_ss<true>(tmem + acc * acc_cols, ad + (kk >> 2) * (kAtomBytes / 16) + 2 * (kk & 3),
+                           bd + (kk >> 2) * (a.H * 8) + 2 * (kk & 3), idesc, kk != 0);
         }
         mma_commit(&empty[slot]);
         mma_commit(&s_full[acc]);
         i = i + kIssuers < kTiles ? i + kIssuers : i + kIssuers - kTiles;
         slot += kIssuers;
-        if (slot >= a.slots) {
-          slot -= a.slots;
+        if (slot >= R::slots) {
+          slot -= R::slots;
           phase ^= 1;
         }
         acc += kIssuers;
-        if (acc >= kAccs) {
-          acc -= kAccs;
+        if (acc >= R::accs) {
+          acc -= R::accs;
           aphase ^= 1;
         }
       }
       if (!ok) *abort_flag = 1;
       // drain, also after a failed wait: the query's copy has landed and no MMA
       // still reads shared memory or writes TMEM
-      mbar_wait(q_full, 0, a.err, kDrainLimitNs);
+      if constexpr (!kKv8) mbar_wait(q_full, 0, a.err, kDrainLimitNs);
       mma_commit(mma_drain);
       mbar_wait(mma_drain, 0, a.err, kDrainLimitNs);
     }
@@ -404,16 +366,15 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   } else if (warp < kSumWarps && nblk > 0) {
     // ---------------------------------------------------------------- sums
     const int wg = warp >> 2, r = threadIdx.x & 127;  // half of the heads, row of the block
-    const int heads = a.hg >> 1, h0 = wg * heads;
+    const int heads = a.H >> 1, h0 = wg * heads;
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h0;
     const float inv_h = 1.f / (float)a.H, most = (float)heads * inv_h;  // powers of two
     bool ok = __all_sync(0xffffffffu, mbar_wait(ready, 0, a.err, a.wait_ns));
     if constexpr (kKv8) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err, a.wait_ns));
-      if (ok) query_to_f16(smem, L.q_atom, a.hg, a.c_hi, a.c_lo, head);
-      fence_proxy_async_smem();  // the MMAs read the query through the async proxy
+      query_to_e4m3(a.q + (int64_t)t * a.H * kDQK, smem, a.H, a.c_hi, a.c_lo, head);
+      fence_proxy_async_smem();  // the MMAs read the terms through the async proxy
       sums_sync();               // the factors that other threads wrote
-      if (lane == 0) mbar_arrive(q_half);
+      if (lane == 0) mbar_arrive(q_full);
     }
     int acc = 0, aphase = 0;
     for (int j = 0; j < nblk; ++j) {
@@ -428,27 +389,43 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
         ok = ok && __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[acc], aphase, a.err, a.wait_ns));
         if (ok) {
           tc_fence_after();
-          uint32_t v[CH][32];  // fewer than 32 heads: the other columns are read and left out below
+          const uint32_t at = t_lane + acc * acc_cols;
+          // fewer than 32 heads: the other columns are read and left out below
+          if constexpr (kKv8) {
+            const float s1 = tile_scale((i < kTiles - 1 ? tiles.x >> (8 * i) : tiles.y) & 0xFFu), s2 = s1 * 0x1p-5f;
 #pragma unroll
-          for (int c = 0; c < CH; ++c) tmem_ld32(t_lane + acc * acc_cols + 32 * c, v[c]);
+            for (int c = 0; c < CH; ++c) {
+              uint32_t v1[32], v2[32];
+              tmem_ld32(at + 32 * c, v1);
+              if constexpr (CH == 1) tmem_ld32(at + a.H + 32 * c, v2);
+              tmem_ld_wait_regs(v1);
 #pragma unroll
-          for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(v[c]);
-          const float sc = kKv8 ? tile_scale((i < kTiles - 1 ? tiles.x >> (8 * i) : tiles.y) & 0xFFu) : 1.f;
+              for (int e = 0; e < 32; ++e)
+                x[c][e] = i == 0 ? __uint_as_float(v1[e]) * s1 : fmaf(__uint_as_float(v1[e]), s1, x[c][e]);
+              if constexpr (CH == 2) tmem_ld32(at + a.H + 32 * c, v2);  // 64 logits leave registers for one term
+              tmem_ld_wait_regs(v2);
 #pragma unroll
-          for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __uint_as_float(v[c][e]);
-              if constexpr (kKv8)
-                x[c][e] = i == 0 ? y * sc : fmaf(y, sc, x[c][e]);
-              else
-                x[c][e] = i == 0 ? y : x[c][e] + y;
+              for (int e = 0; e < 32; ++e) x[c][e] = fmaf(__uint_as_float(v2[e]), s2, x[c][e]);
             }
+          } else {
+            uint32_t v[CH][32];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) tmem_ld32(at + 32 * c, v[c]);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(v[c]);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = __uint_as_float(v[c][e]);
+                x[c][e] = i == 0 ? y : x[c][e] + y;
+              }
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[acc]);
         }
-        if (++acc == kAccs) {
+        if (++acc == R::accs) {
           acc = 0;
           aphase ^= 1;
         }
@@ -501,7 +478,6 @@ int mass_splits(int T, int K) {
 
 template <bool kKv8, int CH>
 cudaError_t launch(const CUtensorMap& tq, MassArgs a, cudaStream_t st) {
-  using R = Roles<kKv8, CH>;
   static thread_local int attr_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -511,16 +487,15 @@ cudaError_t launch(const CUtensorMap& tq, MassArgs a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_dev = dev;
   }
-  a.hg = kKv8 && a.H > 64 ? 64 : a.H;
-  const int T = a.s.num_tokens * (a.H / a.hg), blocks = (a.K + kRows - 1) / kRows;
+  using R = Ring<kKv8, CH>;
+  const int T = a.s.num_tokens, blocks = (a.K + kRows - 1) / kRows;
   const int sp = mass_splits(T, a.K), per = (blocks + sp - 1) / sp;
   a.ks = per * kRows;
   a.splits = (blocks + per - 1) / per;
-  a.slots = R::slots;
   const int64_t ctas = (int64_t)T * a.splits;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(R::threads),
-                    (size_t)(Layout(a.hg, a.slots, R::ahead * R::groups, a.ks).total + 1024), st, tq, a);
+  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(kThreads),
+                    (size_t)(Layout(a.H, R::slots * R::slot_bytes, a.ks).total + 1024), st, tq, a);
 }
 
 }  // namespace
@@ -529,13 +504,13 @@ cudaError_t launch_attn_mass(const SeqsDev& s, const __nv_bfloat16* q, const voi
                              const int32_t* idx, int K, int H, float scale, const float* lse, int64_t* mass,
                              int64_t ld, uint32_t* err, cudaStream_t st) {
   CUtensorMap tq;
-  if (!make_bf16_rows_map(&tq, q, kDQK, (uint64_t)s.num_tokens * H, kv8_scale && H > 64 ? 64 : H)) return cudaErrorInvalidValue;
+  if (!make_bf16_rows_map(&tq, q, kDQK, (uint64_t)s.num_tokens * H, H)) return cudaErrorInvalidValue;
   const double c = (double)scale * 1.4426950408889634;
   const float c_hi = (float)c;
-  const MassArgs a{s, static_cast<const uint8_t*>(kv), kv8_scale, idx, lse, reinterpret_cast<unsigned long long*>(mass),
-                   ld, K, H, 0, 0, 0, 0, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
-  cudaError_t e = kv8_scale ? launch<true, 1>(tq, a, st)
-                            : (H == 128 ? launch<false, 2>(tq, a, st) : launch<false, 1>(tq, a, st));
+  const MassArgs a{s, q, static_cast<const uint8_t*>(kv), kv8_scale, idx, lse, reinterpret_cast<unsigned long long*>(mass),
+                   ld, K, H, 0, 0, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
+  cudaError_t e = H == 128 ? (kv8_scale ? launch<true, 2>(tq, a, st) : launch<false, 2>(tq, a, st))
+                           : (kv8_scale ? launch<true, 1>(tq, a, st) : launch<false, 1>(tq, a, st));
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }

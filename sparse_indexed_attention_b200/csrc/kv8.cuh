@@ -37,18 +37,6 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 codes, float sc) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Eight E4M3 codes as eight fp16 values (exact).
-__device__ __forceinline__ uint4 e4m3x8_to_f16x8(uint2 codes) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? codes.x : codes.y;
-    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-    o[i] = *reinterpret_cast<const uint32_t*>(&hr);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // 2^x from the MUFU unit (approximate, subnormal results flushed to 0;
 // ex2(-inf) = +0).
 __device__ __forceinline__ float ex2_ftz(float x) {
