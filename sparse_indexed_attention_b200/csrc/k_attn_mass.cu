@@ -311,21 +311,25 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
     __syncwarp();
   } else if (warp >= kMmaWarp && warp < kLoadWarp && nblk > 0) {
     // ---------------------------------------------------------------- MMA issuers
-    if (lane == 0) {
+    // The whole warp runs the loop and one elected lane issues: control and operands
+    // stay uniform, which the issue of an MMA wants (operands in uniform registers).
+    {
       const uint32_t idesc = make_idesc(!kKv8, kRows, cols);  // bf16, or E4M3 (kind::f8f6f4)
-      bool ok = mbar_wait(q_full, 0, a.err, a.wait_ns);
+      const int first = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;
+      bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err, a.wait_ns));
       if constexpr (kKv8) fence_proxy_async_smem();  // the terms were written by the summing warps
-      int i = warp - kMmaWarp;  // tile of the block
+      int i = first;  // tile of the block
       int slot = i, phase = 0, acc = i, aphase = 0;
-      for (int it = i; it < nblk * kTiles; it += kIssuers) {
-        ok = ok && !*abort_flag && mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns) &&
-             mbar_wait(&full[slot], phase, a.err, a.wait_ns);
+      for (int it = first; it < nblk * kTiles; it += kIssuers) {
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag && mbar_wait(&s_empty[acc], aphase ^ 1, a.err, a.wait_ns) &&
+                                         mbar_wait(&full[slot], phase, a.err, a.wait_ns));
         if (!ok) break;
         fence_proxy_async_smem();  // the rows were written by cp.async (generic proxy)
         tc_fence_after();
         // descriptors move by bytes / 16: 32 bytes inside the swizzled rows, or an atom
         const uint64_t ad = sw128_kmajor_desc(smem_u32(smem + L.ring + slot * R::slot_bytes));
         const bool last = i == kTiles - 1;
+        if (elect_one()) {
         if constexpr (kKv8) {
           const uint32_t at = smem_u32(smem + i * cols * 128);
           const uint64_t bd = last ? sw64_kmajor_desc(at) : sw128_kmajor_desc(at);
@@ -343,6 +347,8 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
         }
         mma_commit(&empty[slot]);
         mma_commit(&s_full[acc]);
+        }
+        __syncwarp();
         i = i + kIssuers < kTiles ? i + kIssuers : i + kIssuers - kTiles;
         slot += kIssuers;
         if (slot >= R::slots) {
@@ -359,7 +365,8 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       // drain, also after a failed wait: the query's copy has landed and no MMA
       // still reads shared memory or writes TMEM
       if constexpr (!kKv8) mbar_wait(q_full, 0, a.err, kDrainLimitNs);
-      mma_commit(mma_drain);
+      if (elect_one()) mma_commit(mma_drain);
+      __syncwarp();
       mbar_wait(mma_drain, 0, a.err, kDrainLimitNs);
     }
     __syncwarp();
