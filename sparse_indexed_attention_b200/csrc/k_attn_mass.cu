@@ -383,13 +383,24 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       sums_sync();               // the factors that other threads wrote
       if (lane == 0) mbar_arrive(q_full);
     }
+    // this thread's row of a block: pool row, position and (FP8 cache) tile scales
+    int row_next = -1, s_next = 0;
+    uint2 tiles_next = make_uint2(0u, 0u);
+    auto row_of = [&](int j) {
+      const int k = j * kRows + r;
+      row_next = rows[k];
+      if (row_next >= 0) {
+        s_next = __ldg(a.idx + (int64_t)t * a.K + kbeg + k);
+        if constexpr (kKv8) tiles_next = ld_nc_v2(a.kv_scale + (int64_t)row_next * 8);
+      }
+    };
+    if (ok) row_of(0);
     int acc = 0, aphase = 0;
     for (int j = 0; j < nblk; ++j) {
-      const int k = j * kRows + r;
-      const bool live = ok && rows[k] >= 0;
-      const int s = live ? __ldg(a.idx + (int64_t)t * a.K + kbeg + k) : 0;
-      uint2 tiles = make_uint2(0u, 0u);  // FP8 cache: the row's tile scales
-      if constexpr (kKv8) tiles = live ? ld_nc_v2(a.kv_scale + (int64_t)rows[k] * 8) : tiles;
+      const bool live = ok && row_next >= 0;
+      const int s = s_next;
+      const uint2 tiles = tiles_next;
+      if (j + 1 < nblk) row_of(j + 1);  // its loads' latency overlaps this block
       float x[CH][32];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
