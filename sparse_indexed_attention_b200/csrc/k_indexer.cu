@@ -8,11 +8,11 @@
 //
 // As a GEMM per (token group, key tile): D[s, (t,h)] = sum_d K[s,d] Q[(t,h),d]
 // with M = 128 keys (two 64-row pages), N = 64 heads x TG tokens, K = 128.
-//  * warp 0, one lane: TMA producer.  Each key tile is two TMA loads of one
+//  * warp 0: TMA producer.  Each key tile is two TMA loads of one
 //    8 KB page each, straight from the paged pool (the page table is read
 //    here), plus a 256-byte bulk copy of each page's row scales.  The group's
 //    quantized query rows and head weights are loaded once per group.
-//  * warp 1, one lane: issues tcgen05.mma (kind::f8f6f4 E4M3, or kind::f16
+//  * warp 1: issues tcgen05.mma (kind::f8f6f4 E4M3, or kind::f16
 //    bf16) into a ring of TMEM accumulators; tcgen05.commit frees the stage
 //    and publishes the accumulator.
 //  * MXFP8 cache ([P2] section 5 table, "Indexer Q/K": one shared scale per
@@ -609,7 +609,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       cp_async_commit();
     }
     int stage = 0, sphase = 0, prev_g = -1, gcount = 0;
-    int issued = 0, b_issued = 0;  // tiles / group operand loads with copies in flight or landed (lane 0)
+    int issued = 0, b_issued = 0;  // tiles / group operand loads (lane 0) with copies in flight or landed
     bool ok = true;
     for (int it = it_lo; it < it_hi && ok; ++it) {
       // groups so far: the page ids of it_lo .. it_lo+kPgAhead-1, then one
@@ -662,63 +662,49 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         prev_g = cb.z;
         ++gcount;
       }
+      // the whole warp takes each tile's steps; lanes 0 and 1 hold its two pages
+      const int h = lane & 1, last = grp.w + grp.z - 1;
       for (int tile = cb.x; tile < cb.y; ++tile) {
-        const int j = tile - cb.x;
-        const int pg0 = __shfl_sync(0xffffffffu, pages, 2 * j);
-        const int pg1 = __shfl_sync(0xffffffffu, pages, 2 * j + 1);
-        const int last = grp.w + grp.z - 1;
-        int t_ok = 0;
-        if (lane == 0 && !*abort_flag) {
-          if (!mbar_wait(&empty[stage], sphase ^ 1, a.err, a.wait_ns)) {
-            *abort_flag = 1;
+        const int pg = __shfl_sync(0xffffffffu, pages, 2 * (tile - cb.x) + h);
+        const bool wanted = (tile * 2 + h) * kPage <= last, valid = pg >= 0 && pg < a.s.num_phys_pages;
+        const uint32_t live = __ballot_sync(0xffffffffu, wanted && valid) & 3u;  // bit h: page h is loaded
+        if (wanted && !valid && lane < 2) raise_error(a.err, kErrBadIndex);
+        if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&empty[stage], sphase ^ 1, a.err, a.wait_ns))) {
+          *abort_flag = 1;
+          break;
+        }
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(live) *
+                                                  ((uint32_t)(C::A_BYTES / 2) + ((kBf16 || kMx) ? 0u : 256u)));
+        ++issued;
+        __syncwarp();
+        uint8_t* adst = smem + C::OFF_A + stage * C::A_BYTES;
+        if (lane < 2 && wanted && valid) {
+          if constexpr (kBf16) {
+            tma_load_2d(adst + h * 8192, &tmap_k, &full[stage], 0, pg * kPage);
+            tma_load_2d(adst + 16384 + h * 8192, &tmap_k, &full[stage], 64, pg * kPage);
           } else {
-            t_ok = 1;
-            int rows[2];
-            const int pg[2] = {pg0, pg1};
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              rows[h] = -1;
-              if ((tile * 2 + h) * kPage <= last) {
-                if (pg[h] >= 0 && pg[h] < a.s.num_phys_pages) {
-                  rows[h] = pg[h] * kPage;
-                  bytes += (uint32_t)(C::A_BYTES / 2) + ((kBf16 || kMx) ? 0u : 256u);
-                } else {
-                  raise_error(a.err, kErrBadIndex);
-                }
-              }
-            }
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            ++issued;
-            uint8_t* adst = smem + C::OFF_A + stage * C::A_BYTES;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (rows[h] < 0) continue;
-              if constexpr (kBf16) {
-                tma_load_2d(adst + h * 8192, &tmap_k, &full[stage], 0, rows[h]);
-                tma_load_2d(adst + 16384 + h * 8192, &tmap_k, &full[stage], 64, rows[h]);
-              } else {
-                tma_load_2d(adst + h * (C::A_BYTES / 2), &tmap_k, &full[stage], 0, rows[h]);
-                if constexpr (!kMx)
-                  bulk_load(smem + C::OFF_SC + stage * 512 + h * 256, a.kI_scale + rows[h], 256, &full[stage]);
-              }
-            }
+            tma_load_2d(adst + h * (C::A_BYTES / 2), &tmap_k, &full[stage], 0, pg * kPage);
+            if constexpr (!kMx)
+              bulk_load(smem + C::OFF_SC + stage * 512 + h * 256, a.kI_scale + (int64_t)pg * kPage, 256, &full[stage]);
           }
         }
         if constexpr (kMx) {
           // the tile's key scales: key 32 c + l (page c / 2, row 32 (c % 2) + l)
           // goes to row l, column c; every lane arrives once its copies land
-          if (__shfl_sync(0xffffffffu, t_ok, 0)) {
-            uint8_t* sfa = smem + C::OFF_SC + stage * 512;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int h = c >> 1;
-              const int pgh = h ? pg1 : pg0;
-              if ((tile * 2 + h) * kPage <= last && pgh >= 0 && pgh < a.s.num_phys_pages)
-                cp_async_4(sfa + lane * 16 + c * 4, a.kI_sf + ((int64_t)pgh * kPage + 32 * (c & 1) + lane) * 4);
-            }
-            cp_async_mbar_arrive(&full[stage]);
+          const int other = __shfl_xor_sync(0xffffffffu, pg, 1);
+          uint8_t* sfa = smem + C::OFF_SC + stage * 512 + lane * 16;
+          const uint8_t* sf0 = a.kI_sf + ((int64_t)(h ? other : pg) * kPage + lane) * 4;
+          const uint8_t* sf1 = a.kI_sf + ((int64_t)(h ? pg : other) * kPage + lane) * 4;
+          if (live & 1u) {
+            cp_async_4(sfa, sf0);
+            cp_async_4(sfa + 4, sf0 + 128);
           }
+          if (live & 2u) {
+            cp_async_4(sfa + 8, sf1);
+            cp_async_4(sfa + 12, sf1 + 128);
+          }
+          cp_async_mbar_arrive(&full[stage]);
         }
         if (++stage == C::NS) { stage = 0; sphase ^= 1; }
       }
@@ -736,71 +722,87 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the loop and one elected lane issues: control and
+      // operands stay uniform, which the issue of an MMA wants.
       int stage = 0, sphase = 0, acc = 0, aphase = 0, prev_g = -1, gcount = 0, slot = 0;
       int4 nb = it_lo < it_hi ? recs[2 * it_lo + 1] : make_int4(0, 0, 0, 0);
       for (int it = it_lo; it < it_hi && !*abort_flag; ++it) {
         const int4 item = make_int4(nb.z, nb.x, nb.y, 0);  // {g, tile_begin, tile_end}
         if (it + 1 < it_hi) nb = recs[2 * it + 3];
         if (item.x != prev_g) {
-          if (prev_g >= 0) mma_commit(&b_empty[slot]);  // previous group's operands free once its MMAs finish
+          if (prev_g >= 0 && elect_one()) mma_commit(&b_empty[slot]);  // previous group's operands free once its MMAs finish
           slot = gcount & 1;
-          if (!mbar_wait(&b_full[slot], (gcount >> 1) & 1, a.err, a.wait_ns)) { *abort_flag = 1; break; }
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, mbar_wait(&b_full[slot], (gcount >> 1) & 1, a.err, a.wait_ns))) {
+            *abort_flag = 1;
+            break;
+          }
           if constexpr (kMx) {  // the group's query scales into TMEM (in order before its MMAs)
             fence_proxy_async_smem();  // written by cp.async (generic proxy)
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int cp = 0; cp < C::SFB_COPIES; ++cp)
-              tmem_cp_32x128b_x4(tmem + C::SFB0 + slot * C::SFB_COLS + 4 * cp,
-                                 rows16_desc(smem_u32(smem + C::OFF_SFB + slot * C::SFB_BYTES + cp * 512)));
+              for (int cp = 0; cp < C::SFB_COPIES; ++cp)
+                tmem_cp_32x128b_x4(tmem + C::SFB0 + slot * C::SFB_COLS + 4 * cp,
+                                   rows16_desc(smem_u32(smem + C::OFF_SFB + slot * C::SFB_BYTES + cp * 512)));
+            }
+            __syncwarp();
           }
           prev_g = item.x;
           ++gcount;
         }
         const uint32_t b_base = smem_u32(smem + C::OFF_B + slot * C::B_BYTES);
         for (int tile = item.y; tile < item.z; ++tile) {
-          if (!mbar_wait(&full[stage], sphase, a.err, a.wait_ns)) { *abort_flag = 1; break; }
-          if (!mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns)) { *abort_flag = 1; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], sphase, a.err, a.wait_ns) &&
+                                           mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns))) {
+            *abort_flag = 1;
+            break;
+          }
           tc_fence_after();
+          if constexpr (kMx) fence_proxy_async_smem();  // the scales were written by cp.async (generic proxy)
           const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
-          if constexpr (kMx) {
-            // the tile's key scales into TMEM, then (MXFP8) one block-scaled MMA
-            // per 32-wide K block, byte k of each scale column
-            fence_proxy_async_smem();  // written by cp.async (generic proxy)
-            tmem_cp_32x128b_x4(tmem + C::SFA0 + 4 * stage, rows16_desc(smem_u32(smem + C::OFF_SC + stage * 512)));
-            if constexpr (kMx4) {  // one MMA per 64 of the 128 dims: bytes 0, 1 and 2, 3 of each scale column
+          if (elect_one()) {
+            if constexpr (kMx) {
+              // the tile's key scales into TMEM, then one block-scaled MMA per 64
+              // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
+              tmem_cp_32x128b_x4(tmem + C::SFA0 + 4 * stage, rows16_desc(smem_u32(smem + C::OFF_SC + stage * 512)));
+              if constexpr (kMx4) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_mx4(tmem + acc * C::N, sw64_kmajor_desc(a_base + k * 32), sw64_kmajor_desc(b_base + k * 32),
-                        make_idesc_mx4(128, C::N, 2 * k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)(2 * k) << 30),
-                        (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
+                for (int k = 0; k < 2; ++k)
+                  mma_mx4(tmem + acc * C::N, sw64_kmajor_desc(a_base + k * 32), sw64_kmajor_desc(b_base + k * 32),
+                          make_idesc_mx4(128, C::N, 2 * k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)(2 * k) << 30),
+                          (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
+                         make_idesc_mx(128, C::N, k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)k << 30),
+                         (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+              }
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
-                       make_idesc_mx(128, C::N, k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)k << 30),
-                       (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+              for (int k = 0; k < C::KSTEPS; ++k) {
+                // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
+                const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
+                const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
+                mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
+                              C::IDESC, k > 0);
+              }
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < C::KSTEPS; ++k) {
-              // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
-              const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
-              const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
-              mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
-                            C::IDESC, k > 0);
-            }
+            mma_commit(&empty[stage]);
+            mma_commit(&acc_full[acc]);
           }
-          mma_commit(&empty[stage]);
-          mma_commit(&acc_full[acc]);
+          __syncwarp();
           if (++stage == C::NS) { stage = 0; sphase ^= 1; }
           if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
         }
       }
       // drain, also after a failed wait: no MMA of this CTA still reads shared
       // memory or writes TMEM when the CTA deallocates and exits
-      mma_commit(mma_drain);
+      if (elect_one()) mma_commit(mma_drain);
+      __syncwarp();
       mbar_wait(mma_drain, 0, a.err, kDrainLimitNs);
     }
     __syncwarp();
