@@ -8,7 +8,7 @@
 //
 // As a GEMM per (token group, key tile): D[s, (t,h)] = sum_d K[s,d] Q[(t,h),d]
 // with M = 128 keys (two 64-row pages), N = 64 heads x TG tokens, K = 128.
-//  * warp 0: TMA producer.  Each key tile is two TMA loads of one
+//  * warps 0 and 3: TMA producers, alternate tiles (bf16 cache: warp 0 alone).  Each key tile is two TMA loads of one
 //    8 KB page each, straight from the paged pool (the page table is read
 //    here), plus a 256-byte bulk copy of each page's row scales.  The group's
 //    quantized query rows and head weights are loaded once per group.
@@ -99,6 +99,11 @@ struct IdxCfg {
   static constexpr int B_BYTES = N * ROW;
   static constexpr int KSTEPS = kBf16 ? 8 : 4;             // 32-byte K steps per tile
   static constexpr int NS = kBf16 ? 3 : (kMx4 ? (kFused ? 8 : 12) : (TG == 1 ? (kFused ? 6 : 8) : 6));
+  // Two producer warps take alternate tiles: one warp's steps for a tile (waits,
+  // barrier arithmetic, TMA and scale copies) outlast the tile's transfer.  An even
+  // ring gives each stage to one of them, which waits for its uses in order (a
+  // barrier's parity tells the next phase from this one only).
+  static constexpr int NPROD = NS % 2 == 0 && !kFused ? 2 : 1;
   // Accumulator ring.  NACC is even: the two epilogue warpgroups take
   // alternate tiles, so each accumulator (and its barriers) belongs to one
   // warpgroup and is waited on one phase at a time.  MXFP8 also keeps scale
@@ -119,7 +124,7 @@ struct IdxCfg {
   static constexpr int OFF_SFB = OFF_W + 2 * TG * 256;    // MXFP8: 2 x the group's query scales
   static constexpr int OFF_HIST = OFF_SFB + 2 * SFB_BYTES;  // TG == 1: per-epilogue-warp Top-K histograms
   static constexpr int OFF_RING = OFF_HIST + ((TG == 1 && !kFused) ? kEpiWarps * kTopkHistBins * 4 : 0);
-  static constexpr int OFF_BAR = OFF_RING + kRingSlots * (32 + 128);  // producer's item records + page ids
+  static constexpr int OFF_BAR = OFF_RING + NPROD * kRingSlots * (32 + 128);  // producers' item records + page ids
   static constexpr int NBARS = 2 * NS + 4 + 2 * NACC + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
   static constexpr int OFF_TAIL = (OFF_MISC + 16 + 15) / 16 * 16;     // fused: selection scratch
@@ -576,8 +581,9 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
   const int4* recs = a.plan.items;  // item i: recs[2i] = {b, t0, cnt, pos0}, recs[2i+1] = {tile_begin, tile_end, g, 0}
 
-  if (warp == 0) {
+  if (warp == 0 || (C::NPROD == 2 && warp == 3)) {
     // ------------------------------------------------------------ producer (whole warp)
+    const int prod = warp == 0 ? 0 : 1;
     // Item records are fetched kRecAhead items ahead and each item's page ids
     // (one lane per page, <= 32 pages per item) kPgAhead items ahead, as
     // asynchronous copies into a ring in shared memory: one commit group per
@@ -587,8 +593,9 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       prefetch_tmap(&tmap_k);
       prefetch_tmap(&tmap_q);
     }
-    int4* ring_rec = reinterpret_cast<int4*>(smem + C::OFF_RING);                     // [slot][2]
-    int* ring_pg = reinterpret_cast<int*>(smem + C::OFF_RING + kRingSlots * 32);     // [slot][32]
+    uint8_t* ring = smem + C::OFF_RING + prod * kRingSlots * (32 + 128);
+    int4* ring_rec = reinterpret_cast<int4*>(ring);                     // [slot][2]
+    int* ring_pg = reinterpret_cast<int*>(ring + kRingSlots * 32);     // [slot][32]
     auto issue_rec = [&](int it) {
       if (it < it_hi && lane < 2) cp_async_16(&ring_rec[(it % kRingSlots) * 2 + lane], recs + 2 * it + lane);
     };
@@ -609,7 +616,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       cp_async_commit();
     }
     int stage = 0, sphase = 0, prev_g = -1, gcount = 0;
-    int issued = 0, b_issued = 0;  // tiles / group operand loads (lane 0) with copies in flight or landed
+    int issued = 0, b_issued = 0;  // tiles passed (this producer's are issued) / group operand loads (lane 0)
     bool ok = true;
     for (int it = it_lo; it < it_hi && ok; ++it) {
       // groups so far: the page ids of it_lo .. it_lo+kPgAhead-1, then one
@@ -623,7 +630,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const int4 ca = ring_rec[(it % kRingSlots) * 2], cb = ring_rec[(it % kRingSlots) * 2 + 1];
       const int pages = ring_pg[(it % kRingSlots) * 32 + lane];  // lanes past the item's pages are unused
       const int4 grp = ca;  // {b, t0, cnt, pos0}
-      if (cb.z != prev_g) {
+      if (prod == 0 && cb.z != prev_g) {
         const int slot = gcount & 1, use = gcount >> 1;
         int b_ok = 0;
         if (lane == 0) {
@@ -665,6 +672,11 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       // the whole warp takes each tile's steps; lanes 0 and 1 hold its two pages
       const int h = lane & 1, last = grp.w + grp.z - 1;
       for (int tile = cb.x; tile < cb.y; ++tile) {
+        if (C::NPROD == 2 && (issued & 1) != prod) {  // the other producer's tile
+          ++issued;
+          if (++stage == C::NS) { stage = 0; sphase ^= 1; }
+          continue;
+        }
         const int pg = __shfl_sync(0xffffffffu, pages, 2 * (tile - cb.x) + h);
         const bool wanted = (tile * 2 + h) * kPage <= last, valid = pg >= 0 && pg < a.s.num_phys_pages;
         const uint32_t live = __ballot_sync(0xffffffffu, wanted && valid) & 3u;  // bit h: page h is loaded
@@ -716,7 +728,8 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     // last use is its only phase that can still be pending)
     if (lane == 0) {
       for (int i = issued > C::NS ? issued - C::NS : 0; i < issued; ++i)
-        if (!mbar_wait(&full[i % C::NS], (uint32_t)((i / C::NS) & 1), a.err, kDrainLimitNs)) break;
+        if ((C::NPROD == 1 || (i & 1) == prod) &&
+            !mbar_wait(&full[i % C::NS], (uint32_t)((i / C::NS) & 1), a.err, kDrainLimitNs)) break;
       for (int i = b_issued > 2 ? b_issued - 2 : 0; i < b_issued; ++i)
         if (!mbar_wait(&b_full[i & 1], (uint32_t)((i >> 1) & 1), a.err, kDrainLimitNs)) break;
     }
