@@ -55,11 +55,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kEpiWarps = 8;                 // two epilogue warpgroups (warps 4-11)
 constexpr int kRingSlots = 8;                // producer's look-ahead ring (items)
 constexpr int kRecAhead = 6;                 // item records are fetched this many items ahead
 constexpr int kPgAhead = 3;                  // page ids this many items ahead
-constexpr int kIdxThreads = (4 + kEpiWarps) * 32;
 
 constexpr int kTailRuns = 32;                // rows a CTA can hold parts of (fused selection)
 constexpr int kTailItemsMax = 32;            // items a CTA can keep the scores of (fused selection)
@@ -98,12 +96,20 @@ struct IdxCfg {
   static constexpr int A_BYTES = 128 * ROW;                // 128 keys x d_I
   static constexpr int B_BYTES = N * ROW;
   static constexpr int KSTEPS = kBf16 ? 8 : 4;             // 32-byte K steps per tile
-  static constexpr int NS = kBf16 ? 3 : (kMx4 ? (kFused ? 8 : 12) : (TG == 1 ? (kFused ? 6 : 8) : 6));
+  static constexpr int NS = kBf16 ? 3 : (kMx4 ? (TG == 1 ? 8 : 12) : (TG == 1 ? (kFused ? 6 : 8) : 6));
   // Two producer warps take alternate tiles: one warp's steps for a tile (waits,
   // barrier arithmetic, TMA and scale copies) outlast the tile's transfer.  An even
   // ring gives each stage to one of them, which waits for its uses in order (a
   // barrier's parity tells the next phase from this one only).
   static constexpr int NPROD = NS % 2 == 0 && !kFused ? 2 : 1;
+  // Epilogue warpgroups (from warp 4).  MXFP4 tiles come twice as fast, so four
+  // warpgroups share them: with one token per group each takes every fourth tile, with
+  // two each takes one token of every other tile.
+  static constexpr int NWG = kMx4 && !kFused ? 4 : 2;
+  static constexpr int EPI = 4 * NWG;                      // warps
+  static constexpr int THREADS = (4 + EPI) * 32;
+  static constexpr int TILE_WGS = TG == 1 ? NWG : 2;       // tile i -> the warpgroups that are i mod TILE_WGS
+  static constexpr int TOKEN_WGS = NWG / TILE_WGS;         // which then take the group's tokens in turn
   // Accumulator ring.  NACC is even: the two epilogue warpgroups take
   // alternate tiles, so each accumulator (and its barriers) belongs to one
   // warpgroup and is waited on one phase at a time.  MXFP8 also keeps scale
@@ -123,7 +129,7 @@ struct IdxCfg {
   // (MXFP8: the OFF_SC area holds each stage's key scales in the scale-factor layout, 512 B)
   static constexpr int OFF_SFB = OFF_W + 2 * TG * 256;    // MXFP8: 2 x the group's query scales
   static constexpr int OFF_HIST = OFF_SFB + 2 * SFB_BYTES;  // TG == 1: per-epilogue-warp Top-K histograms
-  static constexpr int OFF_RING = OFF_HIST + ((TG == 1 && !kFused) ? kEpiWarps * kTopkHistBins * 4 : 0);
+  static constexpr int OFF_RING = OFF_HIST + ((TG == 1 && !kFused) ? EPI * kTopkHistBins * 4 : 0);
   static constexpr int OFF_BAR = OFF_RING + NPROD * kRingSlots * (32 + 128);  // producers' item records + page ids
   static constexpr int NBARS = 2 * NS + 4 + 2 * NACC + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
@@ -136,7 +142,7 @@ struct IdxCfg {
   static constexpr int SMEM = BYTES + 1024;                // slack for 1024-byte alignment
   static constexpr uint32_t IDESC = make_idesc(kBf16, 128, N);
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(NACC * N <= TMEM_COLS && NACC % 2 == 0, "TMEM accumulators (an even number)");
+  static_assert(NACC * N <= TMEM_COLS && NACC % TILE_WGS == 0, "each TMEM accumulator belongs to its warpgroups");
   static_assert(!kMx || SFB0 + 2 * SFB_COLS <= TMEM_COLS, "TMEM scale columns");
   static_assert(OFF_SFB % 512 == 0, "scale-factor sources need 16-byte alignment");
   static_assert(!kFused || CAP_ITEMS >= 8, "fused selection capacity");
@@ -510,6 +516,23 @@ __device__ void fused_topk_tail(const IdxArgs& a, uint32_t* keys, int it_lo, int
   }
 }
 
+__device__ __forceinline__ float relu(uint32_t bits) { return fmaxf(__uint_as_float(bits), 0.f); }
+
+// {a0, a1} * {b0, b1} + c as two fp32 lanes of one instruction.
+__device__ __forceinline__ uint64_t fma2(float a0, float a1, float b0, float b1, uint64_t c) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "fma.rn.f32x2 %0, a, b, %5;\n\t}"
+      : "=l"(d)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
 // Adds one epilogue warp's histogram of the current token to the global one
 // and clears it (warp-private, so only the warp synchronises).
 __device__ __forceinline__ void flush_hist(uint32_t* sh, uint32_t* gh, int t, int lane) {
@@ -525,7 +548,7 @@ __device__ __forceinline__ void flush_hist(uint32_t* sh, uint32_t* gh, int t, in
 }
 
 template <bool kBf16, int TG, bool kFused, bool kMx, bool kMx4>
-__global__ void __launch_bounds__(kIdxThreads, 1)
+__global__ void __launch_bounds__((IdxCfg<kBf16, TG, kFused, kMx, kMx4>::THREADS), 1)
 k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q,
                   const IdxArgs a) {
   using C = IdxCfg<kBf16, TG, kFused, kMx, kMx4>;
@@ -549,15 +572,15 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     // MXFP8: the producer's 32 lanes also arrive, once their scale copies land
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&full[i], kMx ? 1 + 32 : 1);
-      mbar_init(&empty[i], 1 + 4);
+      mbar_init(&empty[i], kMx ? 1 : 1 + 4);  // MMAs, and the epilogue that reads the stage's row scales
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b_full[i], kMx ? 1 + 32 : 1);
-      mbar_init(&b_empty[i], 1 + kEpiWarps);
+      mbar_init(&b_empty[i], 1 + C::EPI);
     }
     for (int i = 0; i < C::NACC; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 4 * C::TOKEN_WGS);
     }
     mbar_init(mma_drain, 1);
     *abort_flag = 0;
@@ -822,13 +845,14 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     // Two warpgroups take alternate tiles (tile i -> warpgroup i & 1, which
-    // therefore owns every other TMEM accumulator); both follow every group.
+    // therefore owns every other TMEM accumulator; four share them for the
+    // MXFP4 cache, see NWG); all follow every group.
     const int q = (warp - 4) & 3;      // TMEM lane quarter of this warp
     const int wg = (warp - 4) >> 2;    // epilogue warpgroup
     const int r = q * 32 + lane;       // key row of the tile
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
     int stage = 0, sphase = 0, acc = 0, aphase = 0, prev_g = -1, gcount = 0, slot = 0, prev_t = -1, ti = 0;
-    float wreg[64];
+    float wreg[C::NWG == 2 && TG == 1 ? 64 : 1];  // (more warpgroups leave no registers for the weights)
     uint32_t* sh_hist = reinterpret_cast<uint32_t*>(smem + C::OFF_HIST) + (warp - 4) * kTopkHistBins;
     const bool do_hist = TG == 1 && !kFused && a.hist != nullptr;
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem + C::OFF_KEYS);
@@ -854,7 +878,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           *abort_flag = 1;
           break;
         }
-        if constexpr (TG == 1) {
+        if constexpr (C::NWG == 2 && TG == 1) {
 #pragma unroll
           for (int h = 0; h < 64; ++h) wreg[h] = w_smem[slot * TG * 64 + h];
         }
@@ -862,40 +886,57 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         ++gcount;
       }
       for (int tile = item.y; tile < item.z; ++tile, ++ti) {
-        if ((ti & 1) == wg) {
+        if (ti % C::TILE_WGS == wg % C::TILE_WGS) {
           bool okw = mbar_wait(&acc_full[acc], aphase, a.err, a.wait_ns);
           // the row scales arrived with the stage's TMA; observe that completion here too
-          if (!kBf16) okw = okw && mbar_wait(&full[stage], sphase, a.err, a.wait_ns);
+          if (!kBf16 && !kMx) okw = okw && mbar_wait(&full[stage], sphase, a.err, a.wait_ns);
           if (!__all_sync(0xffffffffu, okw)) { *abort_flag = 1; break; }
           tc_fence_after();
           const float sk = (kBf16 || kMx) ? 1.f : sc_smem[stage * 128 + r];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[stage]);
+          if constexpr (!kMx) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+          }
           const int s = tile * 128 + r;
 #pragma unroll 1
-          for (int k = 0; k < TG; ++k) {
+          for (int k = wg / C::TILE_WGS; k < TG; k += C::TOKEN_WGS) {
             uint32_t v0[32], v1[32];
             tmem_ld32(t_lane + acc * C::N + k * 64, v0);
             tmem_ld32(t_lane + acc * C::N + k * 64 + 32, v1);
             tmem_ld_wait_regs(v0);
             tmem_ld_wait_regs(v1);
-            if (k == TG - 1) {  // every TMEM read of this accumulator is complete
+            if (k + C::TOKEN_WGS >= TG) {  // every TMEM read of this accumulator is complete
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&acc_empty[acc]);
             }
             const float* wk = w_smem + slot * TG * 64 + k * 64;
             float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;  // four chains instead of one
+            if constexpr (kMx4) {
+              // two products per instruction (packed fp32), four weights per load
+              uint64_t a01 = 0, a23 = 0;
 #pragma unroll
-            for (int h = 0; h < 32; h += 2) {
-              const float w0 = TG == 1 ? wreg[h] : wk[h];
-              const float w1 = TG == 1 ? wreg[h + 1] : wk[h + 1];
-              const float w2 = TG == 1 ? wreg[h + 32] : wk[h + 32];
-              const float w3 = TG == 1 ? wreg[h + 33] : wk[h + 33];
-              p0 = fmaf(w0, fmaxf(__uint_as_float(v0[h]), 0.f), p0);
-              p1 = fmaf(w1, fmaxf(__uint_as_float(v0[h + 1]), 0.f), p1);
-              p2 = fmaf(w2, fmaxf(__uint_as_float(v1[h]), 0.f), p2);
-              p3 = fmaf(w3, fmaxf(__uint_as_float(v1[h + 1]), 0.f), p3);
+              for (int h = 0; h < 32; h += 4) {
+                const float4 wa = *reinterpret_cast<const float4*>(wk + h), wb = *reinterpret_cast<const float4*>(wk + 32 + h);
+                a01 = fma2(wa.x, wa.y, relu(v0[h]), relu(v0[h + 1]), a01);
+                a23 = fma2(wb.x, wb.y, relu(v1[h]), relu(v1[h + 1]), a23);
+                a01 = fma2(wa.z, wa.w, relu(v0[h + 2]), relu(v0[h + 3]), a01);
+                a23 = fma2(wb.z, wb.w, relu(v1[h + 2]), relu(v1[h + 3]), a23);
+              }
+              unpack2(a01, p0, p1);
+              unpack2(a23, p2, p3);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 32; h += 2) {
+                const float w0 = TG == 1 ? wreg[h] : wk[h];
+                const float w1 = TG == 1 ? wreg[h + 1] : wk[h + 1];
+                const float w2 = TG == 1 ? wreg[h + 32] : wk[h + 32];
+                const float w3 = TG == 1 ? wreg[h + 33] : wk[h + 33];
+                p0 = fmaf(w0, fmaxf(__uint_as_float(v0[h]), 0.f), p0);
+                p1 = fmaf(w1, fmaxf(__uint_as_float(v0[h + 1]), 0.f), p1);
+                p2 = fmaf(w2, fmaxf(__uint_as_float(v1[h]), 0.f), p2);
+                p3 = fmaf(w3, fmaxf(__uint_as_float(v1[h + 1]), 0.f), p3);
+              }
             }
             const float score = ((p0 + p1) + (p2 + p3)) * sk;
             const bool valid = k < grp.z && s <= grp.w + k;
@@ -923,14 +964,14 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
   if (TG == 1 && !kFused && a.hist != nullptr && !*abort_flag && it_hi > it_lo) {
-    // the last token's histogram: the eight warps' copies summed here and
+    // the last token's histogram: the warps' copies summed here and
     // added once per CTA (earlier tokens were flushed per warp as they ended)
     const int t_last = recs[2 * (it_hi - 1)].y;
     const uint32_t* hb = reinterpret_cast<const uint32_t*>(smem + C::OFF_HIST);
     for (int i = threadIdx.x; i < kTopkHistBins; i += blockDim.x) {
       uint32_t v = 0;
 #pragma unroll
-      for (int w = 0; w < kEpiWarps; ++w) v += hb[w * kTopkHistBins + i];
+      for (int w = 0; w < C::EPI; ++w) v += hb[w * kTopkHistBins + i];
       if (v) atomicAdd(a.hist + (int64_t)t_last * kTopkHistBins + i, v);
     }
   }
@@ -982,7 +1023,7 @@ cudaError_t launch_tc(const CUtensorMap& mk, const CUtensorMap& mq, const IdxArg
     attr_dev = dev;
   }
   cudaError_t e = launch_pdl("index_scores", k_index_scores_tc<kBf16, TG, kFused, kMx, kMx4>, dim3(grid),
-                             dim3(kIdxThreads), (size_t)C::SMEM, st, mk, mq, a);
+                             dim3(C::THREADS), (size_t)C::SMEM, st, mk, mq, a);
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }
