@@ -25,9 +25,12 @@
 //    the MMA lane moves them into TMEM with tcgen05.cp (32 rows x 128 bits,
 //    written to every lane quarter) ahead of the tile's MMAs.  The epilogue
 //    is that of the E4M3 cache without the key scale.
-//  * MXFP4 cache: the same with packed E2M1 codes, rows of 64 bytes in the
-//    64-byte swizzle, and kind::mxf4 (two MMAs of 64 dims per tile): half the
-//    bytes of a key and twice the tensor rate.
+//  * MXFP4 cache: the same with packed E2M1 codes (64-byte rows) and kind::mxf4
+//    (two MMAs of 64 dims per tile): half the bytes of a key and twice the tensor
+//    rate.  A TMA load moves a swizzled row per request, and rows of 64 bytes
+//    bound the kernel by requests; so a page is loaded as 32 rows of two keys, and a
+//    stage holds 256 keys: its even keys are the first halves of 128 rows in the
+//    128-byte swizzle, its odd keys the second halves, each the A operand of a tile.
 //  * warp 2: allocates and frees TMEM.
 //  * warps 4-11: epilogue, two warpgroups taking alternate tiles.  Thread r
 //    of a warpgroup owns TMEM lane r = key row r, so the ReLU, the head
@@ -93,10 +96,12 @@ struct IdxCfg {
   static_assert(kMx || !kMx4, "MXFP4 is an MX cache");
   static constexpr int N = 64 * TG;                        // MMA N: heads x tokens of a group
   static constexpr int ROW = kBf16 ? 256 : (kMx4 ? 64 : 128);  // bytes of an operand row
-  static constexpr int A_BYTES = 128 * ROW;                // 128 keys x d_I
+  static constexpr int SUB = kMx4 ? 2 : 1;                 // tiles of 128 keys per stage (MXFP4: even and odd keys)
+  static constexpr int A_BYTES = SUB * 128 * ROW;          // a stage's keys x d_I
+  static constexpr int PAGES = 2 * SUB;                    // per stage
   static constexpr int B_BYTES = N * ROW;
   static constexpr int KSTEPS = kBf16 ? 8 : 4;             // 32-byte K steps per tile
-  static constexpr int NS = kBf16 ? 3 : (kMx4 ? (TG == 1 ? 8 : 12) : (TG == 1 ? (kFused ? 6 : 8) : 6));
+  static constexpr int NS = kBf16 ? 3 : (kMx4 ? (TG == 1 ? 4 : 8) : (TG == 1 ? (kFused ? 6 : 8) : 6));
   // Two producer warps take alternate tiles: one warp's steps for a tile (waits,
   // barrier arithmetic, TMA and scale copies) outlast the tile's transfer.  An even
   // ring gives each stage to one of them, which waits for its uses in order (a
@@ -118,15 +123,15 @@ struct IdxCfg {
   static constexpr int SFB_COPIES = kMx ? (N + 127) / 128 : 0;   // 32x128b copies per group
   static constexpr int SFB_BYTES = SFB_COPIES * 512;
   static constexpr int SFA0 = NACC * N;                    // TMEM column of stage 0's key scales
-  static constexpr int SFB0 = SFA0 + 4 * NS;               // TMEM column of slot 0's query scales
+  static constexpr int SFB0 = SFA0 + 4 * SUB * NS;               // TMEM column of slot 0's query scales
   static constexpr int SFB_COLS = 4 * SFB_COPIES;
   static constexpr int TMEM_COLS = kMx ? 512 : ((NACC * N) <= 256 ? 256 : 512);
   // shared-memory layout (offsets from a 1024-aligned base)
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + NS * A_BYTES;
   static constexpr int OFF_SC = OFF_B + 2 * B_BYTES;       // NS x 128 fp32 row scales
-  static constexpr int OFF_W = OFF_SC + NS * 512;          // 2 x TG x 64 fp32 head weights
-  // (MXFP8: the OFF_SC area holds each stage's key scales in the scale-factor layout, 512 B)
+  static constexpr int OFF_W = OFF_SC + NS * SUB * 512;    // 2 x TG x 64 fp32 head weights
+  // (MX caches: the OFF_SC area holds each tile's key scales in the scale-factor layout, 512 B)
   static constexpr int OFF_SFB = OFF_W + 2 * TG * 256;    // MXFP8: 2 x the group's query scales
   static constexpr int OFF_HIST = OFF_SFB + 2 * SFB_BYTES;  // TG == 1: per-epilogue-warp Top-K histograms
   static constexpr int OFF_RING = OFF_HIST + ((TG == 1 && !kFused) ? EPI * kTopkHistBins * 4 : 0);
@@ -639,7 +644,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       cp_async_commit();
     }
     int stage = 0, sphase = 0, prev_g = -1, gcount = 0;
-    int issued = 0, b_issued = 0;  // tiles passed (this producer's are issued) / group operand loads (lane 0)
+    int issued = 0, b_issued = 0;  // stages passed (this producer's are issued) / group operand loads (lane 0)
     bool ok = true;
     for (int it = it_lo; it < it_hi && ok; ++it) {
       // groups so far: the page ids of it_lo .. it_lo+kPgAhead-1, then one
@@ -692,39 +697,54 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         prev_g = cb.z;
         ++gcount;
       }
-      // the whole warp takes each tile's steps; lanes 0 and 1 hold its two pages
-      const int h = lane & 1, last = grp.w + grp.z - 1;
-      for (int tile = cb.x; tile < cb.y; ++tile) {
-        if (C::NPROD == 2 && (issued & 1) != prod) {  // the other producer's tile
+      // the whole warp takes each stage's steps; lane h holds its page h
+      const int h = lane & (C::PAGES - 1), last = grp.w + grp.z - 1;
+      for (int tile = cb.x; tile < cb.y; tile += C::SUB) {
+        if (C::NPROD == 2 && (issued & 1) != prod) {  // the other producer's stage
           ++issued;
           if (++stage == C::NS) { stage = 0; sphase ^= 1; }
           continue;
         }
         const int pg = __shfl_sync(0xffffffffu, pages, 2 * (tile - cb.x) + h);
-        const bool wanted = (tile * 2 + h) * kPage <= last, valid = pg >= 0 && pg < a.s.num_phys_pages;
-        const uint32_t live = __ballot_sync(0xffffffffu, wanted && valid) & 3u;  // bit h: page h is loaded
-        if (wanted && !valid && lane < 2) raise_error(a.err, kErrBadIndex);
+        const bool wanted = (tile * 2 + h) * kPage <= last && tile * 2 + h < 2 * cb.y;
+        const bool valid = pg >= 0 && pg < a.s.num_phys_pages;
+        const uint32_t live = __ballot_sync(0xffffffffu, wanted && valid) & ((1u << C::PAGES) - 1u);  // bit h: page h is loaded
+        if (wanted && !valid && lane < C::PAGES) raise_error(a.err, kErrBadIndex);
         if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&empty[stage], sphase ^ 1, a.err, a.wait_ns))) {
           *abort_flag = 1;
           break;
         }
+        constexpr uint32_t kPageBytes = C::A_BYTES / C::PAGES;
         if (lane == 0)
-          mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(live) *
-                                                  ((uint32_t)(C::A_BYTES / 2) + ((kBf16 || kMx) ? 0u : 256u)));
+          mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(live) * (kPageBytes + ((kBf16 || kMx) ? 0u : 256u)));
         ++issued;
         __syncwarp();
         uint8_t* adst = smem + C::OFF_A + stage * C::A_BYTES;
-        if (lane < 2 && wanted && valid) {
+        if (lane < C::PAGES && wanted && valid) {
           if constexpr (kBf16) {
             tma_load_2d(adst + h * 8192, &tmap_k, &full[stage], 0, pg * kPage);
             tma_load_2d(adst + 16384 + h * 8192, &tmap_k, &full[stage], 64, pg * kPage);
           } else {
-            tma_load_2d(adst + h * (C::A_BYTES / 2), &tmap_k, &full[stage], 0, pg * kPage);
+            tma_load_2d(adst + h * kPageBytes, &tmap_k, &full[stage], 0, kMx4 ? pg * (kPage / 2) : pg * kPage);
             if constexpr (!kMx)
               bulk_load(smem + C::OFF_SC + stage * 512 + h * 256, a.kI_scale + (int64_t)pg * kPage, 256, &full[stage]);
           }
         }
-        if constexpr (kMx) {
+        if constexpr (kMx4) {
+          // tile p's row 32 c + l is key 2 l + p of page c: its scales go to row l,
+          // column c of the tile's block; every lane arrives once its copies land
+          uint8_t* sfa = smem + C::OFF_SC + stage * 1024 + lane * 16;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int pc = __shfl_sync(0xffffffffu, pg, c);
+            if (live >> c & 1u) {
+              const uint8_t* src = a.kI_sf + ((int64_t)pc * kPage + 2 * lane) * 4;
+              cp_async_4(sfa + 4 * c, src);
+              cp_async_4(sfa + 512 + 4 * c, src + 4);
+            }
+          }
+          cp_async_mbar_arrive(&full[stage]);
+        } else if constexpr (kMx) {
           // the tile's key scales: key 32 c + l (page c / 2, row 32 (c % 2) + l)
           // goes to row l, column c; every lane arrives once its copies land
           const int other = __shfl_xor_sync(0xffffffffu, pg, 1);
@@ -747,7 +767,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     }
     cp_async_wait<0>();  // no copy into the ring is still in flight at exit
     // drain, also after a failed wait: every copy this warp issued has landed
-    // before the CTA exits (tile i used stage i % NS in phase i / NS; a stage's
+    // before the CTA exits (use i was stage i % NS in phase i / NS; a stage's
     // last use is its only phase that can still be pending)
     if (lane == 0) {
       for (int i = issued > C::NS ? issued - C::NS : 0; i < issued; ++i)
@@ -790,49 +810,56 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           ++gcount;
         }
         const uint32_t b_base = smem_u32(smem + C::OFF_B + slot * C::B_BYTES);
-        for (int tile = item.y; tile < item.z; ++tile) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], sphase, a.err, a.wait_ns) &&
-                                           mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns))) {
+        for (int tile = item.y; tile < item.z; tile += C::SUB) {
+          bool okw = __all_sync(0xffffffffu, mbar_wait(&full[stage], sphase, a.err, a.wait_ns));
+          if constexpr (kMx) fence_proxy_async_smem();  // the scales were written by cp.async (generic proxy)
+          const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
+#pragma unroll
+          for (int p = 0; p < C::SUB && okw; ++p) {
+            okw = __all_sync(0xffffffffu, mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns));
+            if (!okw) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if constexpr (kMx) {
+                // the tile's key scales into TMEM, then one block-scaled MMA per 64
+                // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
+                const uint32_t sfa = tmem + C::SFA0 + 4 * (C::SUB * stage + p);
+                tmem_cp_32x128b_x4(sfa, rows16_desc(smem_u32(smem + C::OFF_SC + (C::SUB * stage + p) * 512)));
+                if constexpr (kMx4) {
+#pragma unroll
+                  for (int k = 0; k < 2; ++k)
+                    mma_mx4(tmem + acc * C::N, sw128_kmajor_desc(a_base + p * 64 + k * 32),
+                            sw64_kmajor_desc(b_base + k * 32), make_idesc_mx4(128, C::N, 2 * k),
+                            sfa | ((uint32_t)(2 * k) << 30),
+                            (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
+                           make_idesc_mx(128, C::N, k), sfa | ((uint32_t)k << 30),
+                           (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < C::KSTEPS; ++k) {
+                  // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
+                  const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
+                  const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
+                  mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
+                                C::IDESC, k > 0);
+                }
+              }
+              if (p == C::SUB - 1) mma_commit(&empty[stage]);
+              mma_commit(&acc_full[acc]);
+            }
+            __syncwarp();
+            if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
+          }
+          if (!okw) {
             *abort_flag = 1;
             break;
           }
-          tc_fence_after();
-          if constexpr (kMx) fence_proxy_async_smem();  // the scales were written by cp.async (generic proxy)
-          const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
-          if (elect_one()) {
-            if constexpr (kMx) {
-              // the tile's key scales into TMEM, then one block-scaled MMA per 64
-              // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
-              tmem_cp_32x128b_x4(tmem + C::SFA0 + 4 * stage, rows16_desc(smem_u32(smem + C::OFF_SC + stage * 512)));
-              if constexpr (kMx4) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  mma_mx4(tmem + acc * C::N, sw64_kmajor_desc(a_base + k * 32), sw64_kmajor_desc(b_base + k * 32),
-                          make_idesc_mx4(128, C::N, 2 * k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)(2 * k) << 30),
-                          (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
-                         make_idesc_mx(128, C::N, k), (tmem + C::SFA0 + 4 * stage) | ((uint32_t)k << 30),
-                         (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < C::KSTEPS; ++k) {
-                // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
-                const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
-                const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
-                mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
-                              C::IDESC, k > 0);
-              }
-            }
-            mma_commit(&empty[stage]);
-            mma_commit(&acc_full[acc]);
-          }
-          __syncwarp();
           if (++stage == C::NS) { stage = 0; sphase ^= 1; }
-          if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
         }
       }
       // drain, also after a failed wait: no MMA of this CTA still reads shared
@@ -885,7 +912,8 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         prev_g = item.x;
         ++gcount;
       }
-      for (int tile = item.y; tile < item.z; ++tile, ++ti) {
+      const int tiles_up = item.z + (item.z - item.y) % C::SUB;  // whole stages
+      for (int tile = item.y; tile < tiles_up; ++tile, ++ti) {
         if (ti % C::TILE_WGS == wg % C::TILE_WGS) {
           bool okw = mbar_wait(&acc_full[acc], aphase, a.err, a.wait_ns);
           // the row scales arrived with the stage's TMA; observe that completion here too
@@ -897,7 +925,8 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[stage]);
           }
-          const int s = tile * 128 + r;
+          // MXFP4: the stage's even keys, then its odd ones
+          const int s = kMx4 ? (tile & ~1) * 128 + 2 * r + (tile & 1) : tile * 128 + r;
 #pragma unroll 1
           for (int k = wg / C::TILE_WGS; k < TG; k += C::TOKEN_WGS) {
             uint32_t v0[32], v1[32];
@@ -943,7 +972,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             if constexpr (kFused) {
               // the host sizes the grid so that a CTA's items fit; the guard keeps
               // an oversized share from writing past the buffer all the same
-              if (it - it_lo < C::CAP_ITEMS) keys[(it - it_lo) * 1024 + (tile - item.y) * 128 + r] = order_key(score);
+              if (it - it_lo < C::CAP_ITEMS) keys[(it - it_lo) * 1024 + s - item.y * 128] = order_key(score);
             } else {
               if (valid) a.scores[(int64_t)(grp.y + k) * a.ld + s] = score;
               // scores fall in random bins: a plain shared-memory add beats aggregating equal bins
@@ -951,7 +980,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             }
           }
         }
-        if (++stage == C::NS) { stage = 0; sphase ^= 1; }
+        if ((tile - item.y) % C::SUB == C::SUB - 1 && ++stage == C::NS) { stage = 0; sphase ^= 1; }
         if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
       }
     }
@@ -987,7 +1016,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 // ---------------------------------------------------------------- host side
 
 // Row-major 2-D map: rows of `row_elems` elements, box of box_x x box_y,
-// 128-byte swizzle (64-byte for the 64-byte rows of MXFP4 codes).
+// 128-byte swizzle (64-byte for the 64-byte rows of MXFP4 queries).
 bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint32_t box_x,
               uint32_t box_y) {
   const bool narrow = !bf16 && row_elems == 64;
@@ -1058,7 +1087,8 @@ cudaError_t launch_index_scores(const SeqsDev& s, const PlanBufs& plan, int tg, 
   const uint64_t qrows = (uint64_t)s.num_tokens * kHI;
   CUtensorMap mk, mq;
   const int row = mx4 ? kDI / 2 : kDI;  // elements (bytes of codes) per row
-  if (!make_map(&mk, kI, bf16, row, R, bf16 ? 64 : row, 64)) return cudaErrorInvalidValue;
+  // (MXFP4 keys: rows of two keys, 32 per page)
+  if (!make_map(&mk, kI, bf16, kDI, mx4 ? R / 2 : R, bf16 ? 64 : kDI, mx4 ? kPage / 2 : kPage)) return cudaErrorInvalidValue;
   if (!make_map(&mq, q_operand, bf16, row, qrows, bf16 ? 64 : row, 64 * tg)) return cudaErrorInvalidValue;
   IdxArgs a{s,
             plan,
