@@ -171,6 +171,7 @@ struct MoveArgs {
   const uint8_t* src[DSA_MAX_POOLS];
   uint8_t* dst[DSA_MAX_POOLS];
   int row_bytes[DSA_MAX_POOLS], vec[DSA_MAX_POOLS];
+  uint32_t magic[DSA_MAX_POOLS];
   const int64_t* mass;
   int64_t* new_mass;
   int64_t ld, new_ld;
@@ -217,40 +218,54 @@ __global__ void __launch_bounds__(1024) k_evict_mark(const MoveArgs a) {
   }
 }
 
+// Rows of V vectors, nv per row: element i of the block's page is vector i % nv of its
+// row i / nv (by a product with `magic` = ceil(2^32 / nv): exact for i < 64 nv, nv <= 2^14).
 template <class V>
-__device__ __forceinline__ void move_rows(const uint8_t* src, uint8_t* dst, int row_bytes, const int* rows, int n) {
-  const int nv = row_bytes / (int)sizeof(V), total = n * nv;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < total; i += kMoveThreads) {
-    const int r = i / nv, c = i - r * nv;
-    const int row = rows[r];
-    if (row >= 0)
-      reinterpret_cast<V*>(dst + (int64_t)r * row_bytes)[c] =
-          __ldg(reinterpret_cast<const V*>(src + (int64_t)row * row_bytes) + c);
+struct RowsOf {
+  const uint8_t* src;
+  uint8_t* dst;
+  int row_bytes, nv, total;
+  uint32_t magic;
+  __device__ __forceinline__ bool load(int i, const int* rows, V* v) const {
+    if (i >= total) return false;
+    const int r = nv == 1 ? i : (int)__umulhi((uint32_t)i, magic), c = i - r * nv, row = rows[r];
+    if (row < 0) return false;
+    *v = __ldg(reinterpret_cast<const V*>(src + (int64_t)row * row_bytes) + c);
+    return true;
+  }
+  __device__ __forceinline__ void store(int i, const V& v) const { reinterpret_cast<V*>(dst)[i] = v; }
+};
+
+// A batch of loads is issued before its stores.
+constexpr int kMoveBatch = 6;
+template <class V>
+__device__ __forceinline__ void move_rows(const RowsOf<V>& m, const int* rows) {
+  for (int i0 = threadIdx.x; i0 < m.total; i0 += kMoveBatch * kMoveThreads) {
+    V v[kMoveBatch];
+    bool in[kMoveBatch];
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u) in[u] = m.load(i0 + u * kMoveThreads, rows, &v[u]);
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u)
+      if (in[u]) m.store(i0 + u * kMoveThreads, v[u]);
   }
 }
 
-// One block: rows 64 p .. 64 p + 63 of sequence b's new cache.
+template <class V>
+__device__ __forceinline__ void move_pool(const MoveArgs& a, int k, int64_t page, const int* rows, int n) {
+  const int nv = a.row_bytes[k] / (int)sizeof(V);
+  move_rows(RowsOf<V>{a.src[k], a.dst[k] + page * kPage * a.row_bytes[k], a.row_bytes[k], nv, n * nv, a.magic[k]}, rows);
+}
+
+// One block: rows 64 p .. 64 p + 63 of sequence b's new cache.  The rows are
+// resolved before the wait for k_evict_mark: what they depend on was complete when
+// that kernel let this one start (it waits for its predecessor first).
 __global__ void __launch_bounds__(kMoveThreads) k_evict_compact(const MoveArgs a) {
   __shared__ int rows[kPage];
   __shared__ int page;
   const int chunks = (a.budget + kPage - 1) / kPage, b = blockIdx.x / chunks, p = blockIdx.x % chunks, tid = threadIdx.x;
-  pdl_wait();
-  pdl_trigger();
   const int kept = rows_to_move(a, b);
-  if (kept < 0 && p == 0 && tid == 0) raise_error(a.err, kErrBadIndex);
   const int n = min(kPage, kept - p * kPage);
-  if (n <= 0) return;
-  if (tid == 0) {
-    const int d = p < a.new_max_pages ? __ldg(a.new_table + (int64_t)b * a.new_max_pages + p) : -1;
-    bool ok = d >= 0 && d < a.new_pages;
-    if (ok) {
-      const uint32_t bit = 1u << (d & 31);
-      ok = !((a.read[d >> 5] | a.twice[d >> 5]) & bit);
-    }
-    if (!ok) raise_error(a.err, kErrBadIndex);
-    page = ok ? d : -1;
-  }
   int s = -1, row = -1;
   if (tid < n) {
     s = __ldg(a.keep + (int64_t)b * a.budget + p * kPage + tid);
@@ -260,18 +275,32 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_compact(const MoveArgs a
       raise_error(a.err, kErrBadIndex);
     rows[tid] = row;
   }
+  int d = -1;
+  if (tid == 0 && n > 0 && p < a.new_max_pages) d = __ldg(a.new_table + (int64_t)b * a.new_max_pages + p);
+  pdl_wait();
+  pdl_trigger();
+  if (kept < 0 && p == 0 && tid == 0) raise_error(a.err, kErrBadIndex);
+  if (n <= 0) return;
+  if (tid == 0) {
+    bool ok = d >= 0 && d < a.new_pages;
+    if (ok) {
+      const uint32_t bit = 1u << (d & 31);
+      ok = !((__ldcg(a.read + (d >> 5)) | __ldcg(a.twice + (d >> 5))) & bit);
+    }
+    if (!ok) raise_error(a.err, kErrBadIndex);
+    page = ok ? d : -1;
+  }
   __syncthreads();
   if (page < 0) return;
   if (a.mass && row >= 0)
     a.new_mass[(int64_t)b * a.new_ld + p * kPage + tid] = __ldg(a.mass + (int64_t)b * a.ld + s);
   for (int k = 0; k < a.npools; ++k) {
-    uint8_t* dst = a.dst[k] + (int64_t)page * kPage * a.row_bytes[k];
     if (a.vec[k] == 16)
-      move_rows<uint4>(a.src[k], dst, a.row_bytes[k], rows, n);
+      move_pool<uint4>(a, k, page, rows, n);
     else if (a.vec[k] == 8)
-      move_rows<uint2>(a.src[k], dst, a.row_bytes[k], rows, n);
+      move_pool<uint2>(a, k, page, rows, n);
     else
-      move_rows<uint32_t>(a.src[k], dst, a.row_bytes[k], rows, n);
+      move_pool<uint32_t>(a, k, page, rows, n);
   }
 }
 
@@ -336,6 +365,8 @@ cudaError_t launch_evict_compact(const SeqsDev& s, const EvictMove& m, void* bit
     a.dst[k] = static_cast<uint8_t*>(p.dst);
     a.row_bytes[k] = p.row_bytes;
     a.vec[k] = p.row_bytes % 16 == 0 ? 16 : (p.row_bytes % 8 == 0 ? 8 : 4);
+    const uint32_t nv = (uint32_t)(p.row_bytes / a.vec[k]);
+    a.magic[k] = nv == 1 ? 0u : (uint32_t)(((1ull << 32) + nv - 1) / nv);
     a.in_place = a.in_place || p.src == p.dst;
   }
   a.mass = m.mass;
