@@ -10,7 +10,7 @@
 // its positions with the keys in shared memory, read from HBM once.  The
 // cluster resolves the budget's key digit by digit (11, 11, 10 bits): every
 // CTA counts its keys, and each sums all the CTAs' histograms through
-// distributed shared memory and finds the same bin.  Counts before each CTA give
+// distributed shared memory (two bins per thread) and finds the same bin by a scan.  Counts before each CTA give
 // the output offsets, so the positions come out ascending.  Latency bound: four
 // cluster barriers and a scan.  MEASURED-SELECT
 //
@@ -52,9 +52,8 @@ struct SelectArgs {
 
 struct SelectSmem {
   uint32_t hist[kD1Bins + kD2Bins + kD3Bins];  // this CTA's counts, one table per digit
-  uint32_t sum[kD1Bins];                       // the cluster's counts of the current digit
   uint32_t buf[33];
-  uint32_t bin, above, gt, eq;
+  uint32_t bin, above, inside, gt, eq;
 };
 
 // kStaged: the CTA's keys fit in shared memory; otherwise each pass reads the
@@ -116,42 +115,60 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const SelectArgs a
       hist_add(hist, digit, in);  // never-attended positions share one bin
     }
     cluster.sync();
-    for (int d = tid; d < bins; d += kSelThreads) {
-      uint32_t v = 0;
-      for (int r = 0; r < C; ++r) v += cluster.map_shared_rank(hist, r)[d];
-      sm.sum[d] = v;
+    // the cluster's counts, from the highest digit down, `pt` digits per thread;
+    // the thread in which the running count reaches `need` holds the digit
+    const int pt = bins / kSelThreads, top = bins - 1 - tid * pt;
+    uint32_t c0 = 0, c1 = 0;
+    for (int r = 0; r < C; ++r) {
+      const uint32_t* h = cluster.map_shared_rank(hist, r);
+      c0 += h[top];
+      if (pt == 2) c1 += h[top - 1];
+    }
+    uint32_t all;
+    uint32_t above = topk::block_scan(c0 + c1, sm.buf, &all);
+    if (above < need && need <= above + c0 + c1) {
+      const bool second = need > above + c0;
+      sm.bin = (uint32_t)(second ? top - 1 : top);
+      sm.above = above + (second ? c0 : 0u);
+      sm.inside = second ? c1 : c0;
     }
     __syncthreads();
-    if (level < 2)
-      topk::find_bin<kD1Bins>(sm.sum, need, &sm.bin, &sm.above);
-    else
-      topk::find_bin<kD3Bins>(sm.sum, need, &sm.bin, &sm.above);
     prefix = (prefix << (level < 2 ? 11 : 10)) | sm.bin;
     need -= sm.above;
+    if (need == sm.inside) {  // the whole bin stays: its lowest key is the border
+      prefix <<= level == 0 ? 21 : (level == 1 ? 10 : 0);
+      need = 0xFFFFFFFFu;
+      break;
+    }
     __syncthreads();
   }
-  // tau: the budget's key; `need` positions that hold exactly tau stay, the lowest
+  // Keys above tau stay, and the `need` lowest positions of those that equal it
+  // (need = 2^32 - 1: all of them, and tau may be lower than any key of its bin).
+  const bool whole = need == 0xFFFFFFFFu;
   const uint32_t tau = prefix;
+  if (tid < 2) (tid == 0 ? sm.gt : sm.eq) = 0u;
+  __syncthreads();
   uint32_t gt = 0, eq = 0;
   for (int i = tid; i < len; i += kSelThreads) {
     const uint32_t key = key_at(i);
     gt += key > tau ? 1u : 0u;
     eq += key == tau ? 1u : 0u;
   }
-  uint32_t total;
-  topk::block_scan(gt, sm.buf, &total);
-  if (tid == 0) sm.gt = total;
-  topk::block_scan(eq, sm.buf, &total);
-  if (tid == 0) sm.eq = total;
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if ((tid & 31) == 0) {
+    atomicAdd(&sm.gt, gt);
+    atomicAdd(&sm.eq, eq);
+  }
   cluster.sync();
   uint32_t gt_before = 0, eq_before = 0;
   for (int r = 0; r < rank; ++r) {
     gt_before += *cluster.map_shared_rank(&sm.gt, r);
     eq_before += *cluster.map_shared_rank(&sm.eq, r);
   }
-  const uint32_t taken = min(eq_before, need), at = gt_before + taken;
+  const uint32_t taken = min(eq_before, need), at = gt_before + taken, left = whole ? 0xFFFFFFFFu : need - taken;
   topk::emit_selected(
-      len, tau, need - taken, a.budget - (int)at, [&](int i) { return make_int2(s0 + i, (int)key_at(i)); }, keep + at,
+      len, tau, left, a.budget - (int)at, [&](int i) { return make_int2(s0 + i, (int)key_at(i)); }, keep + at,
       sm.buf);
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }

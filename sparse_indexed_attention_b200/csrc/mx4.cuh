@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t quantize_piece(const uint4& raw, uint32_t* s
   return finite ? codes : 0u;
 }
 
+// Lane piece's codes and, from one lane in four, the scale to a row.
+__device__ __forceinline__ void store_piece(uint32_t c, uint32_t byte, uint8_t* codes, uint8_t* scales, int64_t row) {
+  const int piece = threadIdx.x & (kPieces - 1);
+  reinterpret_cast<uint32_t*>(codes + row * kRowBytes)[piece] = c;
+  if ((piece & 3) == 0) scales[row * 4 + (piece >> 2)] = (uint8_t)byte;
+}
+
 // One row by 16 neighbouring lanes; `live` false computes without storing.
 __device__ __forceinline__ void quantize_row(const __nv_bfloat16* __restrict__ src, int64_t src_row, uint8_t* codes,
                                              uint8_t* scales, int64_t dst_row, bool live) {
@@ -56,9 +63,7 @@ __device__ __forceinline__ void quantize_row(const __nv_bfloat16* __restrict__ s
   if (live) raw = __ldg(reinterpret_cast<const uint4*>(src + src_row * kDI) + piece);
   uint32_t byte;
   const uint32_t c = quantize_piece(raw, &byte);
-  if (!live) return;
-  reinterpret_cast<uint32_t*>(codes + dst_row * kRowBytes)[piece] = c;
-  if ((piece & 3) == 0) scales[dst_row * 4 + (piece >> 2)] = (uint8_t)byte;
+  if (live) store_piece(c, byte, codes, scales, dst_row);
 }
 
 }  // namespace mx4
