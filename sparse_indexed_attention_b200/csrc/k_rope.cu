@@ -43,6 +43,7 @@ struct RopeArgs {
   int T, H, D, rot, offset;
   int tb, hb;              // tokens and heads per block
   int head_blocks;
+  uint32_t units_magic;    // ceil(2^32 / units), or 0: divide
   bool pos64, transpose, copy;  // copy: dims outside the rotated range are written too
 };
 
@@ -59,11 +60,18 @@ struct alignas(sizeof(E) * VEC) Vec {
   E v[VEC];
 };
 
+template <class E>
+__device__ __forceinline__ void rotate(E& a, E& b, float2 cs) {
+  const float p = to_f(a), q = to_f(b);
+  a = from_f<E>(fmaf(p, cs.x, -q * cs.y));
+  b = from_f<E>(fmaf(p, cs.y, q * cs.x));
+}
+
 // One block: tb tokens x hb heads.  Work units of a (token, head) row: the
 // rotated ones first -- VEC consecutive dims interleaved (VEC = 1: one pair), or a
 // vector of each half -- then the copied vectors of the other dims.
 template <class E, int VEC, bool kHalf>
-__global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) k_rope(const RopeArgs a) {
   __shared__ float2 cs[kMaxAngles];
   using V = Vec<E, VEC>;
   const int half = a.rot >> 1;
@@ -87,39 +95,34 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a) {
   const int units = nrot + (a.copy ? (a.D - a.rot) / VEC : 0);
   const int total = nt * nh * units;
   for (int i = threadIdx.x; i < total; i += kThreads) {
-    const int row = i / units, u = i - row * units;
+    const int row = a.units_magic ? (int)__umulhi((uint32_t)i, a.units_magic) : i / units, u = i - row * units;
     const int k = row / nh, h = row - k * nh;
     const E* x = static_cast<const E*>(a.x) + (t0 + k) * a.xt + (int64_t)(h0 + h) * a.xh;
     E* o = static_cast<E*>(a.out) + (t0 + k) * a.ot + (int64_t)(h0 + h) * a.oh;
-    if (u >= nrot) {
-      int d = (u - nrot) * VEC;
-      if (d >= a.offset) d += a.rot;
-      *reinterpret_cast<V*>(o + d) = *reinterpret_cast<const V*>(x + d);
-      continue;
+    // copied and rotated units share their loads and stores: apart, a warp that
+    // holds both would wait for memory twice
+    constexpr bool kTwo = kHalf || VEC == 1;  // a rotated unit is two vectors: the pairs' first and second elements
+    const bool turn = u < nrot;
+    int d0 = a.offset + (VEC == 1 && !kHalf ? 2 * u : u * VEC);
+    if (!turn) {
+      d0 = (u - nrot) * VEC;
+      if (d0 >= a.offset) d0 += a.rot;
     }
-    const float2* c = cs + k * half + u * kPairVec;
-    if constexpr (kHalf || VEC == 1) {  // vectors (or single dims) of the pairs' first and second elements
-      const int d0 = a.offset + (kHalf ? u * VEC : 2 * u), d1 = d0 + (kHalf ? half : 1);
-      V va = *reinterpret_cast<const V*>(x + d0), vb = *reinterpret_cast<const V*>(x + d1);
+    V va = *reinterpret_cast<const V*>(x + d0), vb;
+    if constexpr (kTwo)
+      if (turn) vb = *reinterpret_cast<const V*>(x + d0 + (kHalf ? half : 1));
+    if (turn) {
+      const float2* c = cs + k * half + u * kPairVec;
+      if constexpr (kTwo) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float p = to_f(va.v[e]), q = to_f(vb.v[e]);
-        va.v[e] = from_f<E>(fmaf(p, c[e].x, -q * c[e].y));
-        vb.v[e] = from_f<E>(fmaf(p, c[e].y, q * c[e].x));
-      }
-      *reinterpret_cast<V*>(o + d0) = va;
-      *reinterpret_cast<V*>(o + d1) = vb;
-    } else {
-      const int d = a.offset + u * VEC;
-      V v = *reinterpret_cast<const V*>(x + d);
+        for (int e = 0; e < VEC; ++e) rotate(va.v[e], vb.v[e], c[e]);
+        *reinterpret_cast<V*>(o + d0 + (kHalf ? half : 1)) = vb;
+      } else {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        const float p = to_f(v.v[2 * e]), q = to_f(v.v[2 * e + 1]);
-        v.v[2 * e] = from_f<E>(fmaf(p, c[e].x, -q * c[e].y));
-        v.v[2 * e + 1] = from_f<E>(fmaf(p, c[e].y, q * c[e].x));
+        for (int e = 0; e < VEC / 2; ++e) rotate(va.v[2 * e], va.v[2 * e + 1], c[e]);
       }
-      *reinterpret_cast<V*>(o + d) = v;
     }
+    *reinterpret_cast<V*>(o + d0) = va;
   }
 }
 
@@ -136,7 +139,7 @@ cudaError_t launch_typed(const RopeArgs& a, bool half_layout, bool vec, unsigned
 cudaError_t launch_rope(const RopeCall& r, cudaStream_t st) {
   const int size = r.dtype == DSA_ROPE_F32 ? 4 : 2, W = 16 / size;
   RopeArgs a{r.x,   r.out, r.xt,  r.xh,     r.ot, r.oh, r.pos, r.turns, r.amp, r.T, r.H, r.D,
-             r.rot, r.offset, 1, r.H, 1, r.pos64, r.transpose, r.x != r.out};
+             r.rot, r.offset, 1, r.H, 1, 0u, r.pos64, r.transpose, r.x != r.out};
   auto ok = [&](int64_t v) { return v % W == 0; };
   const bool vec = (reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.out)) % 16 == 0 && ok(r.xt) &&
                    ok(r.xh) && ok(r.ot) && ok(r.oh) && ok(r.offset) && ok(r.D) &&
@@ -155,6 +158,8 @@ cudaError_t launch_rope(const RopeCall& r, cudaStream_t st) {
     a.tb = (int)(t < most ? t : most);
     if (a.tb > r.T) a.tb = r.T;
   }
+  // i / units by a product: exact while i units < 2^32 (a block has at most 1024 + units units)
+  if (units > 1 && units <= 16384) a.units_magic = (uint32_t)(((1ull << 32) + units - 1) / units);
   a.head_blocks = (r.H + a.hb - 1) / a.hb;
   const int64_t grid = ((int64_t)r.T + a.tb - 1) / a.tb * a.head_blocks;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
