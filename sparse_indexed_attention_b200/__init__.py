@@ -624,15 +624,17 @@ def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=No
         for t in (src,) if dst is src else (src, dst):
             if not isinstance(t, torch.Tensor) or t.dim() < 1:
                 raise TypeError(f"pools[{i}]: expected a tensor of rows")
-        row = src.shape[1:]
-        _need(src, f"pools[{i}]", (src.dtype,), (src.shape[0], *row), dev, pages * 64)
+        n_src = src.shape[0]
+        if n_src < pages * 64 or not src.is_contiguous() or src.device != dev:
+            _need(src, f"pools[{i}]", (src.dtype,), tuple(src.shape), dev, pages * 64)
         here = pages
         if dst is not src:
-            _need(dst, f"pools[{i}] destination", (src.dtype,), (dst.shape[0], *row), dev, 64)
+            _need(dst, f"pools[{i}] destination", (src.dtype,), (dst.shape[0], *src.shape[1:]), dev, 64)
             here = dst.shape[0] // 64
         new_pages = here if new_pages is None else min(new_pages, here)
-        cp[i].src, cp[i].dst = src.data_ptr(), dst.data_ptr()
-        cp[i].row_bytes = src.numel() // src.shape[0] * src.element_size()
+        c_pool = cp[i]
+        c_pool.src, c_pool.dst = src.data_ptr(), dst.data_ptr()
+        c_pool.row_bytes = src.stride(0) * src.element_size()
     new_pages = pages if new_pages is None else new_pages
     ld = new_ld = 0
     if mass is not None or new_mass is not None:
