@@ -162,8 +162,8 @@ def _need(t, name: str, dtypes, shape, device: torch.device, min_rows: int = 0):
     otherwise be read out of bounds."""
     try:  # fast path: one pass over the metadata, no message building
         sz = t.shape
-        if t.dtype in dtypes and t.device == device and t.is_contiguous() and sz[0] >= min_rows \
-                and (sz == shape or _fits(sz, shape)):
+        if t.dtype in dtypes and t.device == device and t.is_contiguous() and (sz == shape or _fits(sz, shape)) \
+                and (min_rows == 0 or sz[0] >= min_rows):
             return
     except (AttributeError, IndexError):
         pass
@@ -205,6 +205,15 @@ _FP8T, _U8T = (torch.uint8, torch.float8_e4m3fn), (torch.uint8,)
 
 
 def _need_seqs(seqs: "Seqs", dev: torch.device):
+    qs, cl, pt = seqs.q_seq_start, seqs.ctx_len, seqs.page_table
+    try:  # fast path
+        B = cl.shape[0]
+        if qs.dtype is torch.int32 and cl.dtype is torch.int32 and pt.dtype is torch.int32 and qs.shape == (B + 1,) \
+                and len(cl.shape) == 1 and pt.shape == (B, pt.shape[-1]) and qs.device == dev and cl.device == dev \
+                and pt.device == dev and qs.is_contiguous() and cl.is_contiguous() and pt.is_contiguous():
+            return
+    except (AttributeError, IndexError):
+        pass
     _need(seqs.q_seq_start, "seqs.q_seq_start", _I32T, (seqs.batch + 1,), dev)
     _need(seqs.ctx_len, "seqs.ctx_len", _I32T, (None,), dev)
     _need(seqs.page_table, "seqs.page_table", _I32T, (seqs.batch, None), dev)
@@ -295,9 +304,9 @@ class Seqs:
         return self.ctx_len.shape[0]
 
     def c(self) -> DsaSeqsC:
-        return DsaSeqsC(self.batch, self.num_q_tokens, 64, self.page_table.shape[1], self.num_phys_pages,
-                        self.max_ctx, self.q_seq_start.data_ptr(), self.ctx_len.data_ptr(),
-                        self.page_table.data_ptr())
+        B, max_pages = self.page_table.shape
+        return DsaSeqsC(B, self.num_q_tokens, 64, max_pages, self.num_phys_pages, self.max_ctx,
+                        self.q_seq_start.data_ptr(), self.ctx_len.data_ptr(), self.page_table.data_ptr())
 
 
 def dsa_workspace_size(op: int, seqs: Seqs | None = None, K: int = 1, H: int = 16, *, rows: int = 0,
