@@ -115,6 +115,9 @@ struct IdxCfg {
   static constexpr int THREADS = (4 + EPI) * 32;
   static constexpr int TILE_WGS = TG == 1 ? NWG : 2;       // tile i -> the warpgroups that are i mod TILE_WGS
   static constexpr int TOKEN_WGS = NWG / TILE_WGS;         // which then take the group's tokens in turn
+  // MMA issuers: one per tile of a stage (warp 2, which owns TMEM, issues the
+  // second one's), since the waits, copies and commits around a tile's MMAs are one chain.
+  static constexpr int NISS = SUB;
   // Accumulator ring.  NACC is even: the two epilogue warpgroups take
   // alternate tiles, so each accumulator (and its barriers) belongs to one
   // warpgroup and is waited on one phase at a time.  MXFP8 also keeps scale
@@ -148,7 +151,8 @@ struct IdxCfg {
   static constexpr uint32_t IDESC = make_idesc(kBf16, 128, N);
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NACC * N <= TMEM_COLS && NACC % TILE_WGS == 0, "each TMEM accumulator belongs to its warpgroups");
-  static_assert(!kMx || SFB0 + 2 * SFB_COLS <= TMEM_COLS, "TMEM scale columns");
+  static_assert(NACC % NISS == 0, "and to its issuer");
+  static_assert(!kMx || SFB0 + 2 * NISS * SFB_COLS <= TMEM_COLS, "TMEM scale columns");
   static_assert(OFF_SFB % 512 == 0, "scale-factor sources need 16-byte alignment");
   static_assert(!kFused || CAP_ITEMS >= 8, "fused selection capacity");
   static_assert(!kFused || CAP_ITEMS * 4096 >= kFastScratch, "fused selection fast-path scratch");
@@ -577,17 +581,17 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     // MXFP8: the producer's 32 lanes also arrive, once their scale copies land
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&full[i], kMx ? 1 + 32 : 1);
-      mbar_init(&empty[i], kMx ? 1 : 1 + 4);  // MMAs, and the epilogue that reads the stage's row scales
+      mbar_init(&empty[i], kMx ? C::NISS : 1 + 4);  // MMAs, and the epilogue that reads the stage's row scales
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b_full[i], kMx ? 1 + 32 : 1);
-      mbar_init(&b_empty[i], 1 + C::EPI);
+      mbar_init(&b_empty[i], C::NISS + C::EPI);
     }
     for (int i = 0; i < C::NACC; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4 * C::TOKEN_WGS);
     }
-    mbar_init(mma_drain, 1);
+    mbar_init(mma_drain, C::NISS);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -777,12 +781,13 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         if (!mbar_wait(&b_full[i & 1], (uint32_t)((i >> 1) & 1), a.err, kDrainLimitNs)) break;
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || (C::NISS == 2 && warp == 2)) {
     {
       // ------------------------------------------------------------ MMA issuer
       // The whole warp runs the loop and one elected lane issues: control and
       // operands stay uniform, which the issue of an MMA wants.
-      int stage = 0, sphase = 0, acc = 0, aphase = 0, prev_g = -1, gcount = 0, slot = 0;
+      const int p = C::NISS == 2 ? __shfl_sync(0xffffffffu, warp, 0) - 1 : 0;  // this issuer's tile of each stage
+      int stage = 0, sphase = 0, acc = p, aphase = 0, prev_g = -1, gcount = 0, slot = 0;
       int4 nb = it_lo < it_hi ? recs[2 * it_lo + 1] : make_int4(0, 0, 0, 0);
       for (int it = it_lo; it < it_hi && !*abort_flag; ++it) {
         const int4 item = make_int4(nb.z, nb.x, nb.y, 0);  // {g, tile_begin, tile_end}
@@ -801,7 +806,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             if (elect_one()) {
 #pragma unroll
               for (int cp = 0; cp < C::SFB_COPIES; ++cp)
-                tmem_cp_32x128b_x4(tmem + C::SFB0 + slot * C::SFB_COLS + 4 * cp,
+                tmem_cp_32x128b_x4(tmem + C::SFB0 + (slot * C::NISS + p) * C::SFB_COLS + 4 * cp,
                                    rows16_desc(smem_u32(smem + C::OFF_SFB + slot * C::SFB_BYTES + cp * 512)));
             }
             __syncwarp();
@@ -810,56 +815,53 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           ++gcount;
         }
         const uint32_t b_base = smem_u32(smem + C::OFF_B + slot * C::B_BYTES);
+        const int sfb = slot * C::NISS + p;  // each issuer copies the group's query scales for itself
         for (int tile = item.y; tile < item.z; tile += C::SUB) {
-          bool okw = __all_sync(0xffffffffu, mbar_wait(&full[stage], sphase, a.err, a.wait_ns));
-          if constexpr (kMx) fence_proxy_async_smem();  // the scales were written by cp.async (generic proxy)
-          const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
-#pragma unroll
-          for (int p = 0; p < C::SUB && okw; ++p) {
-            okw = __all_sync(0xffffffffu, mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns));
-            if (!okw) break;
-            tc_fence_after();
-            if (elect_one()) {
-              if constexpr (kMx) {
-                // the tile's key scales into TMEM, then one block-scaled MMA per 64
-                // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
-                const uint32_t sfa = tmem + C::SFA0 + 4 * (C::SUB * stage + p);
-                tmem_cp_32x128b_x4(sfa, rows16_desc(smem_u32(smem + C::OFF_SC + (C::SUB * stage + p) * 512)));
-                if constexpr (kMx4) {
-#pragma unroll
-                  for (int k = 0; k < 2; ++k)
-                    mma_mx4(tmem + acc * C::N, sw128_kmajor_desc(a_base + p * 64 + k * 32),
-                            sw64_kmajor_desc(b_base + k * 32), make_idesc_mx4(128, C::N, 2 * k),
-                            sfa | ((uint32_t)(2 * k) << 30),
-                            (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
-                           make_idesc_mx(128, C::N, k), sfa | ((uint32_t)k << 30),
-                           (tmem + C::SFB0 + slot * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < C::KSTEPS; ++k) {
-                  // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
-                  const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
-                  const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
-                  mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
-                                C::IDESC, k > 0);
-                }
-              }
-              if (p == C::SUB - 1) mma_commit(&empty[stage]);
-              mma_commit(&acc_full[acc]);
-            }
-            __syncwarp();
-            if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
-          }
-          if (!okw) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], sphase, a.err, a.wait_ns) &&
+                                           mbar_wait(&acc_empty[acc], aphase ^ 1, a.err, a.wait_ns))) {
             *abort_flag = 1;
             break;
           }
+          tc_fence_after();
+          if constexpr (kMx) fence_proxy_async_smem();  // the scales were written by cp.async (generic proxy)
+          const uint32_t a_base = smem_u32(smem + C::OFF_A + stage * C::A_BYTES);
+          if (elect_one()) {
+            if constexpr (kMx) {
+              // the tile's key scales into TMEM, then one block-scaled MMA per 64
+              // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
+              const uint32_t sfa = tmem + C::SFA0 + 4 * (C::SUB * stage + p);
+              tmem_cp_32x128b_x4(sfa, rows16_desc(smem_u32(smem + C::OFF_SC + (C::SUB * stage + p) * 512)));
+              if constexpr (kMx4) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  mma_mx4(tmem + acc * C::N, sw128_kmajor_desc(a_base + p * 64 + k * 32),
+                          sw64_kmajor_desc(b_base + k * 32), make_idesc_mx4(128, C::N, 2 * k),
+                          sfa | ((uint32_t)(2 * k) << 30),
+                          (tmem + C::SFB0 + sfb * C::SFB_COLS) | ((uint32_t)(2 * k) << 30), k > 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_mx(tmem + acc * C::N, sw128_kmajor_desc(a_base + k * 32), sw128_kmajor_desc(b_base + k * 32),
+                         make_idesc_mx(128, C::N, k), sfa | ((uint32_t)k << 30),
+                         (tmem + C::SFB0 + sfb * C::SFB_COLS) | ((uint32_t)k << 30), k > 0);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < C::KSTEPS; ++k) {
+                // K step k: 32 bytes inside a 128-byte swizzle row; bf16 rows span two 128-byte blocks
+                const uint32_t a_off = kBf16 ? (k >> 2) * 16384 + (k & 3) * 32 : k * 32;
+                const uint32_t b_off = kBf16 ? (k >> 2) * (C::N * 128) + (k & 3) * 32 : k * 32;
+                mma_ss<kBf16>(tmem + acc * C::N, sw128_kmajor_desc(a_base + a_off), sw128_kmajor_desc(b_base + b_off),
+                              C::IDESC, k > 0);
+              }
+            }
+            mma_commit(&empty[stage]);
+            mma_commit(&acc_full[acc]);
+          }
+          __syncwarp();
           if (++stage == C::NS) { stage = 0; sphase ^= 1; }
+          acc += C::NISS;
+          if (acc >= C::NACC) { acc -= C::NACC; aphase ^= 1; }
         }
       }
       // drain, also after a failed wait: no MMA of this CTA still reads shared
