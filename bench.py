@@ -71,7 +71,9 @@ def ncu_traffic(kernel: str, config: dict):
 
 
 def index_cache(spec) -> str:
-    """The index cache's format; MXFP8 overrides the per-row E4M3 flag."""
+    """The index cache's format; MXFP4 and MXFP8 override the per-row E4M3 flag."""
+    if spec.ki_mx4:
+        return "mxfp4"
     return "mxfp8" if spec.ki_mx else ("fp8_e4m3" if spec.ki_fp8 else "bf16")
 
 
@@ -81,8 +83,8 @@ def data_desc(spec) -> str:
 
 def index_row_bytes(spec) -> int:
     """Index-cache bytes per key: 128 codes + 4 scale bytes (one fp32, or four
-    E8M0 bytes), or 128 bf16 values."""
-    return 256 if index_cache(spec) == "bf16" else 132
+    E8M0 bytes), 64 bytes of packed FP4 codes + 4, or 128 bf16 values."""
+    return {"bf16": 256, "mxfp4": 68}.get(index_cache(spec), 132)
 
 
 def parse():
@@ -101,8 +103,8 @@ def parse():
                     help="one JSON line per workload: fused-call time and the binding roofline of each stage")
     ap.add_argument("--no-all-configs", action="store_true",
                     help="leave out the per-workload summary that a 1-GPU headline line carries")
-    ap.add_argument("--ki", choices=["workload", "mxfp8"], default="workload",
-                    help="index-cache format: the workload's own (E4M3 + row scale for the headline) or MXFP8")
+    ap.add_argument("--ki", choices=["workload", "mxfp8", "mxfp4"], default="workload",
+                    help="index-cache format: the workload's own (E4M3 + row scale for the headline), MXFP8 or MXFP4")
     ap.add_argument("--kv", choices=["bf16", "fp8"], default="bf16",
                     help="latent KV cache: bf16, or FP8 E4M3 with a power-of-two scale per 128-element tile")
     ap.add_argument("--select-in-indexer", action="store_true",
@@ -289,6 +291,8 @@ def bench_spec(args):
     spec = CONFIGS[args.config]
     if args.ki == "mxfp8":
         spec = spec.scaled(ki_mx=True)
+    if args.ki == "mxfp4":
+        spec = spec.scaled(ki_mx4=True)
     if args.kv == "fp8":
         spec = spec.scaled(kv_fp8=True)
     if args.ctx > 0:
@@ -420,7 +424,7 @@ def all_config_lines(args, dsa, dev, stream, flush):
     from dsa_workloads import to_device
     hbm, hbm_src = hbm_peak()
     for name in CONFIGS:
-        spec = CONFIGS[name].scaled(ki_mx=args.ki == "mxfp8", kv_fp8=args.kv == "fp8")
+        spec = CONFIGS[name].scaled(ki_mx=args.ki == "mxfp8", ki_mx4=args.ki == "mxfp4", kv_fp8=args.kv == "fp8")
         wl = make_workload(spec)
         d = to_device(wl)
         T, H, K = wl.T, spec.heads, spec.topk
@@ -643,7 +647,7 @@ def run_ours(args, world, rank, local):
     d2h = h_out.numel() * h_out.element_size() + h_lse.numel() * h_lse.element_size()
 
     cpu = None
-    if rank == 0 and world == 1 and not args.no_cpu_baseline:
+    if rank == 0 and world == 1 and not args.no_cpu_baseline and args.ki != "mxfp4":
         spent, reps = 0.0, 0
         while spent < 10.0:                      # whole batches until ~10 s of host work
             dt, _ = cpu_baseline(wl, T)
@@ -666,7 +670,7 @@ def run_ours(args, world, rank, local):
             "metric": METRIC, "value": value, "unit": "tokens/s", "n_gpus": world, "steps": args.steps,
             "warmup": args.warmup, "ms_per_step": ms, "us_per_call": ms * 1e3, "higher_is_better": True,
             "scaling": "weak", "vs_baseline": None,
-            "dtype": {"mxfp8": "mxfp8", "fp8_e4m3": "fp8-e4m3", "bf16": "bf16"}[index_cache(spec)] + " index / "
+            "dtype": {"mxfp4": "mxfp4", "mxfp8": "mxfp8", "fp8_e4m3": "fp8-e4m3", "bf16": "bf16"}[index_cache(spec)] + " index / "
                      + ("fp8-e4m3 latent, " if spec.kv_fp8 else "") + "bf16 attention / fp32 accum",
             "data": data_desc(spec),
             "config": workload_config(spec, wl, world),
@@ -692,7 +696,11 @@ def main():
     args = parse()
     world, rank, local = dist_setup(args)
     try:
-        if args.impl == "reference":
+        if args.impl == "reference" and args.ki == "mxfp4":
+            if rank == 0:
+                print(json.dumps({"impl": "reference",
+                                  "unavailable": "the timed CPU oracle reads the bf16, E4M3 and MXFP8 index caches"}))
+        elif args.impl == "reference":
             run_reference(args, world, rank)
         else:
             run_ours(args, world, rank, local)

@@ -29,7 +29,9 @@ the order written below):
      row), codes = E4M3(row / scale) by torch's round-to-nearest cast, or as
      MXFP8: E4M3 codes with one E8M0 scale byte per 32 elements, scale
      2^(floor(log2 max|block|) - 8) (2^0 for a zero block), codes =
-     E4M3(block / scale) clamped to +-448, by the same cast; latent KV as bf16
+     E4M3(block / scale) clamped to +-448, by the same cast, or as MXFP4: E2M1
+     codes, two per byte, scale 2^(floor(log2 max|block|) - 2), codes = block /
+     scale rounded to the nearest, ties to even, at most 6; latent KV as bf16
      or as the FP8 cache: per row, tiles of 128 values (the last of 64), each
      with scale 2^e, e the smallest integer with max|tile| <= 448 * 2^e (2^0
      for a zero tile), codes = E4M3(tile / 2^e), scale bytes e + 127 in [R, 8]
@@ -56,6 +58,7 @@ class Spec:
     chunk: tuple = (0, 0)           # chunked: new chunk length range
     ki_fp8: bool = True             # FP8 E4M3 index cache with per-row scale
     ki_mx: bool = False             # MXFP8 index cache (E4M3 + E8M0 per 32 elements); overrides ki_fp8
+    ki_mx4: bool = False            # MXFP4 index cache (E2M1 + E8M0 per 32 elements); overrides both
     kv_fp8: bool = False            # FP8 latent KV cache (E4M3, power-of-two scale per 128-element tile)
     heads: int = 128                # attention query heads
     topk: int = 2048
@@ -96,8 +99,8 @@ class Workload:
     num_phys_pages: int
     qI: torch.Tensor               # bf16 [T, H_I, d_I]
     w: torch.Tensor                # fp32 [T, H_I]
-    kI: torch.Tensor               # uint8 FP8 codes or bf16 [R, d_I]
-    kI_scale: torch.Tensor | None  # fp32 [R] (FP8 cache), uint8 E8M0 [R, 4] (MXFP8) or None
+    kI: torch.Tensor               # uint8 FP8 codes or bf16 [R, d_I], or packed FP4 codes [R, d_I / 2]
+    kI_scale: torch.Tensor | None  # fp32 [R] (FP8 cache), uint8 E8M0 [R, 4] (MXFP8, MXFP4) or None
     q: torch.Tensor                # bf16 [T, H, d_qk]
     kv: torch.Tensor               # bf16 [R, d_qk], or uint8 E4M3 codes [R, d_qk] (FP8 cache)
     planted: list                  # per sequence: np.ndarray of planted positions
@@ -183,6 +186,23 @@ def mx_rows(x: torch.Tensor):
     codes = (blocks * torch.exp2(-e.to(torch.float32))[..., None]).clamp_(-448.0, 448.0)
     codes = codes.to(torch.float8_e4m3fn).view(torch.uint8).reshape(R, d)
     return codes, (e + 127).to(torch.uint8)
+
+
+def mx4_rows(x: torch.Tensor):
+    """Store fp32 rows as MXFP4 (cache format): packed E2M1 codes [R, d/2],
+    element 2i in the low half of byte i, and one E8M0 scale byte per 32 elements."""
+    R, d = x.shape
+    blocks = x.reshape(R, d // 32, 32)
+    amax = blocks.abs().amax(dim=2)
+    _, ex = torch.frexp(amax)
+    e = torch.where(amax > 0, (ex - 3).clamp(-127, 127), torch.zeros_like(ex))
+    y = (blocks * torch.exp2(-e.to(torch.float32))[..., None]).reshape(R, d)
+    # nearest of 0, .5, 1, 1.5, 2, 3, 4, 6: a tie falls to the even code, >= on every second border
+    a, code = y.abs(), torch.zeros((R, d), dtype=torch.uint8)
+    for i, border in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
+        code += (a >= border) if i % 2 else (a > border)
+    code += 8 * ((y < 0) & (code > 0))
+    return (code[:, 0::2] | (code[:, 1::2] << 4)).contiguous(), (e + 127).to(torch.uint8)
 
 
 def make_workload(spec: Spec) -> Workload:
@@ -271,7 +291,13 @@ def make_workload(spec: Spec) -> Workload:
         kv = torch.zeros((R, spec.d_qk), dtype=torch.bfloat16)
         kv[phys_rows] = kv_vals.to(torch.bfloat16)
     del kv_vals
-    if spec.ki_mx:
+    if spec.ki_mx4:
+        codes, sc = mx4_rows(ki_vals)
+        kI = torch.zeros((R, d_I // 2), dtype=torch.uint8)
+        kI[phys_rows] = codes
+        kI_scale = torch.full((R, d_I // 32), 127, dtype=torch.uint8)
+        kI_scale[phys_rows] = sc
+    elif spec.ki_mx:
         codes, sc = mx_rows(ki_vals)
         kI = torch.zeros((R, d_I), dtype=torch.uint8)
         kI[phys_rows] = codes

@@ -133,7 +133,8 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(device: torch.device):
     """The device's current stream, as the integer that ctypes passes on."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 class _Nothing:

@@ -400,7 +400,7 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       const bool live = ok && row_next >= 0;
       const int s = s_next;
       const uint2 tiles = tiles_next;
-      if (j + 1 < nblk) row_of(j + 1);  // its loads' latency overlaps this block
+      if (ok && j + 1 < nblk) row_of(j + 1);  // its loads' latency overlaps this block (after a failed wait: no row ids)
       float x[CH][32];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {

@@ -150,6 +150,78 @@ def test_mass_one_position_from_many_tokens(lib):
 
 
 @pytest.mark.parametrize("kv_fp8", [False, True])
+@pytest.mark.parametrize("heads", [64, 128])
+def test_mass_short_wait_limit_winds_down(lib, heads, kv_fp8):
+    """A wait limit of 1 ns: the kernel gives up by itself and says so (or was
+    fast enough); the next call is clean and right."""
+    wl = make_workload(SMALL["decode_small"].scaled(name=f"limit_{heads}_{kv_fp8}", heads=heads, kv_fp8=kv_fp8))
+    d = to_device(wl)
+    idx = torch.from_numpy(_lists(wl)).cuda()
+    _, lse = lib.dsa_sparse_mla_fwd(d.seqs, d.q, d.kv, idx, wl.scale, kv_scale=d.kv_scale)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+    def run():
+        mass = torch.zeros((wl.spec.batch, wl.max_ctx), dtype=torch.int64, device="cuda")
+        lib.dsa_attn_mass(d.seqs, d.q, d.kv, idx, lse, wl.scale, mass, kv_scale=d.kv_scale, ws=ws)
+        return mass
+    want = run()
+    assert lib.dsa_check_error(ws) == lib.DSA_OK
+    lib.dsa_set_wait_limit_ns(1)
+    try:
+        run()
+    finally:
+        lib.dsa_set_wait_limit_ns(0)
+    assert lib.dsa_check_error(ws) in (lib.DSA_OK, lib.DSA_ERR_TIMEOUT)
+    assert torch.equal(run(), want) and lib.dsa_check_error(ws) == lib.DSA_OK
+
+
+def test_mass_negative_and_zero_scale(lib):
+    wl = make_workload(MASS["decode_h16_fp8"])
+    d = to_device(wl)
+    idx = _lists(wl)
+    for scale in (-0.03, 0.0):
+        _, lse = O.sparse_mla(P.oracle_seqs(wl), bits16(wl.q), P.kv_host(wl), idx, scale)
+        mass = torch.zeros((wl.spec.batch, wl.max_ctx), dtype=torch.int64, device="cuda")
+        lib.dsa_attn_mass(d.seqs, d.q, d.kv, torch.from_numpy(idx).cuda(), torch.from_numpy(lse).float().cuda(), scale,
+                          mass, kv_scale=d.kv_scale)
+        ref = S.attn_mass(P.oracle_seqs(wl), bits16(wl.q), P.kv_host(wl), idx, scale, lse.astype(np.float32), wl.max_ctx)
+        got = mass.cpu().numpy() * UNIT
+        assert np.abs(got - ref).max() <= 2e-3 * ref.max() and np.array_equal(got > 0, ref > 0)
+
+
+def test_mass_query_with_extreme_heads(lib):
+    """FP8 cache: heads of zeros, of subnormals, of huge values, and values far below their head's largest."""
+    wl = make_workload(MASS["decode_h16_fp8"])
+    d = to_device(wl)
+    q = wl.q.clone().double()
+    q[:, 0] = 0.0
+    q[:, 1] *= 2.0 ** -130
+    q[:, 2] *= 2.0 ** -60
+    q[:, 3, 10:] *= 2.0 ** -12
+    q[:, 4, ::2] *= 2.0 ** -20
+    q = q.to(torch.bfloat16)
+    idx = _lists(wl)
+    _, lse = O.sparse_mla(P.oracle_seqs(wl), bits16(q), P.kv_host(wl), idx, wl.scale)
+    lse = lse.astype(np.float32)
+    import dataclasses
+    ref, tol = _reference(dataclasses.replace(wl, q=q), idx, lse)
+    mass = torch.zeros((wl.spec.batch, wl.max_ctx), dtype=torch.int64, device="cuda")
+    args = (d.seqs, q.cuda(), d.kv, torch.from_numpy(idx).cuda())
+    lib.dsa_attn_mass(*args, torch.from_numpy(lse).cuda(), wl.scale, mass, kv_scale=d.kv_scale)
+    # the query's two terms: off by 2^-22 of the head's largest value at most, per dim
+    kv = np.abs(O.kv_rows(P.kv_host(wl), np.arange(wl.num_phys_pages * 64))).sum(1).max()
+    top = float(q.abs().amax(-1).double().max())
+    assert (np.abs(mass.cpu().numpy() * UNIT - ref) <= tol + ref * wl.scale * kv * top * 2.0 ** -22).all()
+    inf = q.clone()
+    inf[0, 5, 7] = float("inf")
+    mass.zero_()
+    lib.dsa_attn_mass(d.seqs, inf.cuda(), d.kv, args[3], torch.from_numpy(lse).cuda(), wl.scale, mass,
+                      kv_scale=d.kv_scale)
+    # the infinite head's half of the heads adds nothing for its token
+    assert mass[0].sum() < 0.8 * 2 ** 40 and abs(int(mass[1].sum()) * UNIT - 1.0) < 2e-3
+
+
+@pytest.mark.parametrize("kv_fp8", [False, True])
 @pytest.mark.parametrize("heads", [16, 64, 128])
 def test_mass_many_blocks_and_waves(lib, heads, kv_fp8):
     """Full lists for more tokens than SMs, again and again: every wait ends, and
@@ -204,9 +276,10 @@ def test_select(lib, n, budget, recent, sink, kind):
     assert np.array_equal(keep.cpu().numpy(), ref)
 
 
-def test_select_past_shared_memory(lib):
+@pytest.mark.parametrize("extra", [-3, 0, 1003])
+def test_select_past_shared_memory(lib, extra):
     """A sequence whose keys do not fit the cluster's shared memory is read again instead."""
-    n, budget = 8 * 40960 + 1003, 100001
+    n, budget = 8 * 40960 + extra, 100001
     mass = _masses(2, n, "heavy")
     ctx = torch.tensor([n, n - 77], dtype=torch.int32)
     keep, lens = lib.dsa_evict_select(ctx.cuda(), mass.cuda(), budget, recent=1000, sink=5)

@@ -57,3 +57,37 @@ def test_format_follows_the_row_size(monkeypatch):
         dsa.dsa_dequantize_mx4(torch.zeros(64, 128, dtype=torch.uint8)[:, :64], sc)
     with pytest.raises(ValueError, match="expected"):
         dsa.dsa_dequantize_mx4(k8, sc)
+
+
+def test_workload_rows_are_mxfp4_encodings():
+    import numpy as np
+
+    from dsa_workloads import CONFIGS, make_workload, mx4_rows
+    from oracle import serving_oracle as S
+    rng = np.random.default_rng(0)
+    x = (rng.standard_normal((50, 128)) * np.exp2(rng.integers(-9, 9, (50, 1)))).astype(np.float32)
+    x[0] = 0.0
+    x[1, :8] = [6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+    x[1, 8:32] = 0.0
+    codes, scales = mx4_rows(torch.from_numpy(x))
+    ref_codes, ref_scales = S.mxfp4_quantize(x)
+    assert np.array_equal(codes.numpy(), ref_codes) and np.array_equal(scales.numpy(), ref_scales)
+    wl = make_workload(CONFIGS["decode_b64_8k_32k"].scaled(batch=2, ctx=(300, 700), ki_mx4=True, planted=8))
+    assert wl.kI.shape == (wl.num_phys_pages * 64, 64) and wl.kI_scale.shape == (wl.num_phys_pages * 64, 4)
+
+
+def test_bench_names_the_format():
+    import bench
+    from dsa_workloads import CONFIGS
+    spec = CONFIGS["decode_b8_128k"].scaled(ki_mx4=True)
+    assert (bench.index_cache(spec), bench.index_row_bytes(spec)) == ("mxfp4", 68)
+
+
+def test_stream_of_a_device_without_an_index(monkeypatch):
+    """\"cuda\" means the current device, as everywhere in torch."""
+    seen = []
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: seen.append(i) or 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    dsa._stream(torch.device("cuda"))
+    dsa._stream(torch.device("cuda", 1))
+    assert seen == [3, 1]
