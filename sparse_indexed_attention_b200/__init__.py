@@ -224,6 +224,14 @@ def _need_ws(ws, dev: torch.device):
     _need(ws, "ws", (torch.uint8,), (None,), dev)
 
 
+def _space(ws, nbytes: int, dev: torch.device, key) -> torch.Tensor:
+    """The caller's workspace, checked, or the cached one."""
+    if ws is None:
+        return workspace(nbytes, dev, key)
+    _need_ws(ws, dev)
+    return ws
+
+
 def _need_index_inputs(seqs: "Seqs", qI, w, kI, kI_scale, check_seqs: bool = True) -> torch.device:
     dev = _cuda_device(qI, "qI")
     T, rows = seqs.num_q_tokens, seqs.num_phys_pages * 64
@@ -380,12 +388,16 @@ def dsa_quantize_index_query_mx4(qI: torch.Tensor, codes=None, scales=None):
     """MXFP4: qI [T, 64, 128] bf16 to packed E2M1 codes uint8 [T, 64, 64] and
     E8M0 scales uint8 [T, 64, 4]."""
     dev = _cuda_device(qI, "qI")
+    _need(qI, "qI", _BF16T, (qI.shape[0], 64, 128), dev)
     T = qI.shape[0]
-    codes = codes if codes is not None else torch.empty((T, 64, 64), dtype=torch.uint8, device=dev)
-    scales = scales if scales is not None else torch.empty((T, 64, 4), dtype=torch.uint8, device=dev)
-    _need(qI, "qI", _BF16T, (T, 64, 128), dev)
-    _need(codes, "codes", _U8T, (T, 64, 64), dev)
-    _need(scales, "scales", _U8T, (T, 64, 4), dev)
+    if codes is None:
+        codes = torch.empty((T, 64, 64), dtype=torch.uint8, device=dev)
+    else:
+        _need(codes, "codes", _U8T, (T, 64, 64), dev)
+    if scales is None:
+        scales = torch.empty((T, 64, 4), dtype=torch.uint8, device=dev)
+    else:
+        _need(scales, "scales", _U8T, (T, 64, 4), dev)
     with _on(dev):
         _check(_lib.dsa_quantize_index_query_mx4(_ptr(qI), T, _ptr(codes), _ptr(scales), _stream(dev)),
                "dsa_quantize_index_query_mx4")
@@ -402,8 +414,7 @@ def dsa_append_index_keys_mx4(seqs: Seqs, k: torch.Tensor, kI: torch.Tensor, kI_
     _need(kI, "kI", _U8T, (None, 64), dev, rows)
     _need(kI_scale, "kI_scale", _U8T, (None, 4), dev, rows)
     c = seqs.c()
-    ws = ws if ws is not None else workspace(256, dev, "append_index_keys")
-    _need_ws(ws, dev)
+    ws = _space(ws, 256, dev, "append_index_keys")
     with _on(dev):
         _check(_lib.dsa_append_index_keys_mx4(ctypes.byref(c), _ptr(k), _ptr(kI), _ptr(kI_scale), _ptr(ws),
                                               ws.numel(), _stream(dev)), "dsa_append_index_keys_mx4")
@@ -415,11 +426,13 @@ def dsa_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None) -> t
     dev = _cuda_device(codes, "codes")
     if codes.dim() < 1 or codes.shape[-1] != 64:
         raise ValueError(f"codes: shape {list(codes.shape)}, expected [..., 64]")
-    lead = tuple(codes.shape[:-1])
-    out = out if out is not None else torch.empty((*lead, 128), dtype=torch.bfloat16, device=dev)
-    _need(codes, "codes", _U8T, (*lead, 64), dev)
+    lead = codes.shape[:-1]
+    _need(codes, "codes", _U8T, codes.shape, dev)
     _need(scales, "scales", _U8T, (*lead, 4), dev)
-    _need(out, "out", _BF16T, (*lead, 128), dev)
+    if out is None:
+        out = torch.empty((*lead, 128), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", _BF16T, (*lead, 128), dev)
     with _on(dev):
         _check(_lib.dsa_dequantize_mx4(_ptr(codes), _ptr(scales), codes.numel() // 64, _ptr(out), _stream(dev)),
                "dsa_dequantize_mx4")
@@ -444,8 +457,7 @@ def dsa_index_scores(seqs: Seqs, qI, w, kI, kI_scale=None, scores=None, ld=None,
     ki_dtype = _ki_dtype(kI_scale, kI)
     c = seqs.c()
     need = _lib.dsa_workspace_size(DSA_OP_INDEX_SCORES, ctypes.byref(c), 1, 16)
-    ws = ws if ws is not None else workspace(need, qI.device, "index_scores")
-    _need_ws(ws, dev)
+    ws = _space(ws, need, dev, "index_scores")
     with _on(dev):
         _check(_lib.dsa_index_scores(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype,
                                      _ptr(scores), ld, _ptr(ws), ws.numel(), _stream(dev)), "dsa_index_scores")
@@ -577,8 +589,7 @@ def dsa_attn_mass(seqs: Seqs, q, kv, idx, lse, scale: float, mass, kv_scale=None
     if mass.shape[1] < seqs.max_ctx:
         raise ValueError(f"mass: {mass.shape[1]} positions per sequence, max_ctx is {seqs.max_ctx}")
     c = seqs.c()
-    ws = ws if ws is not None else workspace(256, dev, "attn_mass")
-    _need_ws(ws, dev)
+    ws = _space(ws, 256, dev, "attn_mass")
     with _on(dev):
         _check(_lib.dsa_attn_mass(ctypes.byref(c), q.data_ptr(), kv.data_ptr(), _ptr(kv_scale),
                                   DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3, idx.data_ptr(), idx.shape[1],
@@ -598,12 +609,15 @@ def dsa_evict_select(ctx_len, mass, budget: int, recent: int = 0, sink: int = 0,
     _need(ctx_len, "ctx_len", _I32T, (B,), dev)
     if budget < 1 or recent < 0 or sink < 0 or recent + sink > budget:
         raise ValueError(f"budget={budget}, recent={recent}, sink={sink}: expected recent + sink <= budget, budget >= 1")
-    keep = keep if keep is not None else torch.empty((B, budget), dtype=torch.int32, device=dev)
-    keep_len = keep_len if keep_len is not None else torch.empty((B,), dtype=torch.int32, device=dev)
-    _need(keep, "keep", _I32T, (B, budget), dev)
-    _need(keep_len, "keep_len", _I32T, (B,), dev)
-    ws = ws if ws is not None else workspace(256, dev, "evict_select")
-    _need_ws(ws, dev)
+    if keep is None:
+        keep = torch.empty((B, budget), dtype=torch.int32, device=dev)
+    else:
+        _need(keep, "keep", _I32T, (B, budget), dev)
+    if keep_len is None:
+        keep_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _need(keep_len, "keep_len", _I32T, (B,), dev)
+    ws = _space(ws, 256, dev, "evict_select")
     with _on(dev):
         _check(_lib.dsa_evict_select(ctx_len.data_ptr(), B, ld, mass.data_ptr(), ld, budget, recent, sink,
                                      keep.data_ptr(), keep_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
@@ -654,8 +668,7 @@ def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=No
     c = seqs.c()
     need = 256 + (3 * ((new_pages + 31) // 32) * 4 + 255) // 256 * 256
     # one cached buffer per size: a captured call's buffer is never replaced by a larger one
-    ws = ws if ws is not None else workspace(need, dev, ("evict_compact", need))
-    _need_ws(ws, dev)
+    ws = _space(ws, need, dev, ("evict_compact", need))
     with _on(dev):
         _check(_lib.dsa_evict_compact(ctypes.byref(c), keep.data_ptr(), keep_len.data_ptr(), keep.shape[1],
                                       new_page_table.data_ptr(), new_page_table.shape[1], new_pages, cp, n, _ptr(mass),
