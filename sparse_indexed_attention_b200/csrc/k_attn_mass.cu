@@ -84,11 +84,14 @@ struct Layout {
   __host__ __device__ Layout(int H, int ring_bytes, int ks) {
     ring = kAtoms * H * 128;
     rows = ring + ring_bytes;
-    head = rows + ks * 4;                  // and 32 entries more: chunks of 32 heads are read whole
+    head = rows + ks * 4;                  // and 32 entries more: chunks of heads are read whole
     bars = head + H * 16 + 512;
     total = bars + (2 * kMaxSlots + 2 * kMaxAccs + 5) * 8 + 16;
   }
 };
+
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&v)[32]) { tmem_ld32(at, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&v)[16]) { tmem_ld16(at, v); }
 
 // A barrier of the summing warps.
 __device__ __forceinline__ void sums_sync() {
@@ -170,8 +173,9 @@ struct Ring {
   static_assert(slots % kIssuers == 0 && accs % kIssuers == 0 && slots <= kMaxSlots && accs <= kMaxAccs, "see above");
 };
 
-// CH: chunks of 32 heads that a summing thread holds (two for H = 128).
-template <bool kKv8, int CH>
+// CH: chunks of W heads that a summing thread holds (2 x 32 for H = 128, 32 for 64, 16
+// for fewer).
+template <bool kKv8, int CH, int W>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
   using R = Ring<kKv8, CH>;
@@ -401,40 +405,40 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
       const int s = s_next;
       const uint2 tiles = tiles_next;
       if (ok && j + 1 < nblk) row_of(j + 1);  // its loads' latency overlaps this block (after a failed wait: no row ids)
-      float x[CH][32];
+      float x[CH][W];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
         ok = ok && __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&s_full[acc], aphase, a.err, a.wait_ns));
         if (ok) {
           tc_fence_after();
           const uint32_t at = t_lane + acc * acc_cols;
-          // fewer than 32 heads: the other columns are read and left out below
+          // fewer than W heads: the other columns are read and left out below
           if constexpr (kKv8) {
             const float s1 = tile_scale((i < kTiles - 1 ? tiles.x >> (8 * i) : tiles.y) & 0xFFu), s2 = s1 * 0x1p-5f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-              uint32_t v1[32], v2[32];
-              tmem_ld32(at + 32 * c, v1);
-              if constexpr (CH == 1) tmem_ld32(at + a.H + 32 * c, v2);
+              uint32_t v1[W], v2[W];
+              tmem_ld(at + W * c, v1);
+              if constexpr (CH == 1) tmem_ld(at + a.H + W * c, v2);
               tmem_ld_wait_regs(v1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < W; ++e)
                 x[c][e] = i == 0 ? __uint_as_float(v1[e]) * s1 : fmaf(__uint_as_float(v1[e]), s1, x[c][e]);
-              if constexpr (CH == 2) tmem_ld32(at + a.H + 32 * c, v2);  // 64 logits leave registers for one term
+              if constexpr (CH == 2) tmem_ld(at + a.H + W * c, v2);  // 64 logits leave registers for one term
               tmem_ld_wait_regs(v2);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[c][e] = fmaf(__uint_as_float(v2[e]), s2, x[c][e]);
+              for (int e = 0; e < W; ++e) x[c][e] = fmaf(__uint_as_float(v2[e]), s2, x[c][e]);
             }
           } else {
-            uint32_t v[CH][32];
+            uint32_t v[CH][W];
 #pragma unroll
-            for (int c = 0; c < CH; ++c) tmem_ld32(at + 32 * c, v[c]);
+            for (int c = 0; c < CH; ++c) tmem_ld(at + W * c, v[c]);
 #pragma unroll
             for (int c = 0; c < CH; ++c) tmem_ld_wait_regs(v[c]);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < W; ++e) {
                 const float y = __uint_as_float(v[c][e]);
                 x[c][e] = i == 0 ? y : x[c][e] + y;
               }
@@ -452,10 +456,10 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float4 h = head[h0 + 32 * c + e];
+        for (int e = 0; e < W; ++e) {
+          const float4 h = head[h0 + W * c + e];
           const float p = ex2_ftz(fmaf(x[c][e], h.z, -h.x) + fmaf(x[c][e], h.w, -h.y));
-          if (32 * c + e < heads) sum[e & 3] += p;
+          if (W * c + e < heads) sum[e & 3] += p;
         }
       // this half's share of the mean over all heads
       const float w = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * inv_h;
@@ -494,14 +498,14 @@ int mass_splits(int T, int K) {
   return best;
 }
 
-template <bool kKv8, int CH>
+template <bool kKv8, int CH, int W>
 cudaError_t launch(const CUtensorMap& tq, MassArgs a, cudaStream_t st) {
   static thread_local int attr_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (attr_dev != dev) {
     cudaError_t e =
-        cudaFuncSetAttribute(k_attn_mass<kKv8, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaFuncSetAttribute(k_attn_mass<kKv8, CH, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     attr_dev = dev;
   }
@@ -512,7 +516,7 @@ cudaError_t launch(const CUtensorMap& tq, MassArgs a, cudaStream_t st) {
   a.splits = (blocks + per - 1) / per;
   const int64_t ctas = (int64_t)T * a.splits;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH>, dim3((unsigned)ctas), dim3(kThreads),
+  return launch_pdl("attn_mass", k_attn_mass<kKv8, CH, W>, dim3((unsigned)ctas), dim3(kThreads),
                     (size_t)(Layout(a.H, R::slots * R::slot_bytes, a.ks).total + 1024), st, tq, a);
 }
 
@@ -527,8 +531,13 @@ cudaError_t launch_attn_mass(const SeqsDev& s, const __nv_bfloat16* q, const voi
   const float c_hi = (float)c;
   const MassArgs a{s, q, static_cast<const uint8_t*>(kv), kv8_scale, idx, lse, reinterpret_cast<unsigned long long*>(mass),
                    ld, K, H, 0, 0, c_hi, (float)(c - c_hi), err, wait_limit_ns()};
-  cudaError_t e = H == 128 ? (kv8_scale ? launch<true, 2>(tq, a, st) : launch<false, 2>(tq, a, st))
-                           : (kv8_scale ? launch<true, 1>(tq, a, st) : launch<false, 1>(tq, a, st));
+  cudaError_t e;
+  if (kv8_scale)
+    e = H == 128 ? launch<true, 2, 32>(tq, a, st) : H == 64 ? launch<true, 1, 32>(tq, a, st) : launch<true, 1, 16>(tq, a, st);
+  else
+    e = H == 128  ? launch<false, 2, 32>(tq, a, st)
+        : H == 64 ? launch<false, 1, 32>(tq, a, st)
+                  : launch<false, 1, 16>(tq, a, st);
   if (e != cudaSuccess) return e;
   return counted(cudaGetLastError());
 }
