@@ -398,9 +398,9 @@ dsa_status_t dsa_index_topk_attn_ex(const dsa_seqs_t *seqs, const void *qI,
 /* Accumulated attention weight, the ranking of cache eviction.  For every query
  * token t of sequence b and every selected position s in idx[t]:
  *   mass[b*ld + s] += 2^40 / H * sum_h exp(scale * q[t,h,:] . KV[s,0:576] - lse[t,h])
- * the weight the token's attention gave s, averaged over heads and limited to
- * [0, 1] (NaN adds nothing), rounded to an integer.  Integer sums: the result
- * does not depend on the order of additions.  q, kv, kv_scale, kv_dtype, idx, K,
+ * the weight the token's attention gave s, averaged over heads.  Each half of the
+ * heads adds its share, limited to [0, 1/2] (NaN adds nothing) and rounded to an
+ * integer.  Integer sums: the result does not depend on the order of additions.  q, kv, kv_scale, kv_dtype, idx, K,
  * H and scale are those of dsa_sparse_mla_fwd_ex, lse its lse.  idx entries of -1
  * add nothing; an entry outside -1..pos(t) is skipped and sets
  * DSA_ERR_BAD_INDEX.

@@ -391,11 +391,11 @@ def dsa_quantize_index_query_mx4(qI: torch.Tensor, codes=None, scales=None):
     _need(qI, "qI", _BF16T, (qI.shape[0], 64, 128), dev)
     T = qI.shape[0]
     if codes is None:
-        codes = torch.empty((T, 64, 64), dtype=torch.uint8, device=dev)
+        codes = qI.new_empty((T, 64, 64), dtype=torch.uint8)
     else:
         _need(codes, "codes", _U8T, (T, 64, 64), dev)
     if scales is None:
-        scales = torch.empty((T, 64, 4), dtype=torch.uint8, device=dev)
+        scales = qI.new_empty((T, 64, 4), dtype=torch.uint8)
     else:
         _need(scales, "scales", _U8T, (T, 64, 4), dev)
     with _on(dev):
@@ -430,7 +430,7 @@ def dsa_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None) -> t
     _need(codes, "codes", _U8T, codes.shape, dev)
     _need(scales, "scales", _U8T, (*lead, 4), dev)
     if out is None:
-        out = torch.empty((*lead, 128), dtype=torch.bfloat16, device=dev)
+        out = codes.new_empty((*lead, 128), dtype=torch.bfloat16)
     else:
         _need(out, "out", _BF16T, (*lead, 128), dev)
     with _on(dev):
@@ -610,11 +610,11 @@ def dsa_evict_select(ctx_len, mass, budget: int, recent: int = 0, sink: int = 0,
     if budget < 1 or recent < 0 or sink < 0 or recent + sink > budget:
         raise ValueError(f"budget={budget}, recent={recent}, sink={sink}: expected recent + sink <= budget, budget >= 1")
     if keep is None:
-        keep = torch.empty((B, budget), dtype=torch.int32, device=dev)
+        keep = mass.new_empty((B, budget), dtype=torch.int32)
     else:
         _need(keep, "keep", _I32T, (B, budget), dev)
     if keep_len is None:
-        keep_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        keep_len = mass.new_empty((B,), dtype=torch.int32)
     else:
         _need(keep_len, "keep_len", _I32T, (B,), dev)
     ws = _space(ws, 256, dev, "evict_select")
@@ -741,7 +741,7 @@ def dsa_rope(x: torch.Tensor, positions: torch.Tensor, table: RopeTable, offset:
     _need(table.turns, "table.turns", (torch.int64,), (table.rot_dim // 2,), dev)
     _need(positions, "positions", (torch.int64, torch.int32), (T,), dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
         ot, oh = H * D if T > 1 else 0, D if H > 1 else 0
     else:
         if out is x:

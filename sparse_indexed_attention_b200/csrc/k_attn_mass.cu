@@ -39,7 +39,11 @@
 // token's whole attention, 8.4 million tokens before it overflows): integer
 // additions commute, so the result does not depend on the order of the atomics.
 //
-// What bounds it: a block's 147 KB of rows against 36 MMAs.  MEASURED
+// What bounds it (warm, one B200): 400 tokens of 2048 rows take 139 us with 128 heads
+// (834 TFLOP/s, 51 % of the measured bf16 rate: MMAs of a tile against its issue, and
+// three waves of CTAs for 2.7) and 96 us with 64 (the gather: 10 TB/s out of L2); over
+// the FP8 cache 64 heads take 115 us (the sums: two terms per head).  A decode step of 8
+// tokens takes 9 us: one block per CTA, the chain of its steps.
 #include "kv8.cuh"
 #include "sm100.cuh"
 #include "tensor_map.cuh"
@@ -481,7 +485,8 @@ k_attn_mass(const __grid_constant__ CUtensorMap tq, const MassArgs a) {
 
 // Slices of a token's list: CTAs run one per SM, each with a start of about
 // two and a half blocks' time (barriers, TMEM, row ids, query), so the cost of a
-// split is its waves times (start + blocks).
+// split is its waves times (start + blocks).  Measured: 8 tokens x 2048 rows take
+// 9.0 us in 16 slices, 26.6 in 2, 47.9 in 1; 400 tokens 137 us in 1, 148 in 2.
 int mass_splits(int T, int K) {
   const int blocks = (K + kRows - 1) / kRows;
   int best = 1;

@@ -12,7 +12,7 @@
 // CTA counts its keys and adds its counts to the bins' owners through distributed
 // shared memory, and each finds the same bin by a scan.  Counts before each CTA give
 // the output offsets, so the positions come out ascending.  Latency bound: four
-// cluster barriers and a scan.  MEASURED-SELECT
+// cluster barriers and the passes over the keys: 8 x 32,768 positions 14 us.
 //
 // mark.  A destination page must be no page that the call reads and no
 // destination twice, or rows would be overwritten while others still read
@@ -21,7 +21,8 @@
 //
 // compact.  A block takes half a destination page of one sequence: 32 rows of
 // every pool, 16 bytes per access where the row size allows.  HBM bound: each
-// kept byte is read once and written once.  MEASURED-COMPACT
+// kept byte is read once and written once: 8 x 8192 rows of 1228 bytes take 36 us
+// with the check of the pages (6 us), 83 % of the measured copy rate in between.
 #include <cooperative_groups.h>
 
 #include "topk_select.cuh"
@@ -370,8 +371,9 @@ cudaError_t launch_evict_select(const int32_t* ctx_len, int B, int max_ctx, cons
                                 int recent, int sink, int32_t* keep, int32_t* keep_len, uint32_t* err,
                                 cudaStream_t st) {
   const SelectArgs a{ctx_len, mass, ld, max_ctx, budget, recent, sink, keep, keep_len, err};
-  // a short row is one CTA's work: its cluster barriers would only add latency
-  const int C = max_ctx <= 4 * kSelThreads ? 1 : kCluster;
+  // a short row is one CTA's work: cluster barriers would only add latency (1000
+  // positions: 9.0 us alone, 10.1 as a cluster; 3001: 11.3 and 10.6; 32,768: 57 and 17)
+  const int C = max_ctx <= 2 * kSelThreads ? 1 : kCluster;
   const int64_t slots = (((int64_t)max_ctx + C - 1) / C + 3) & ~3;
   if (slots > kSlotsMax) return launch_cluster("evict_select", k_evict_select<false>, B * C, C, kSelThreads, 0, st, a);
   static thread_local int attr_dev = -1;

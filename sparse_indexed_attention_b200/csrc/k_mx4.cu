@@ -5,7 +5,8 @@
 // values, 16 bytes per lane on the bf16 side, 4 on the code side, so that a
 // warp's accesses are whole 128-byte lines and the group maximum is two
 // shuffles.  Four rows per thread group: one row each was bound by the start of
-// blocks (4096 x 64 rows: 18.5 us, MEASURED).
+// blocks (4096 x 64 rows: 18.5 us, now 15.4 us for 85 MB, 84 % of the measured copy rate;
+// back: 18.1, now 11.7 us, part of it from L2).
 #include <cuda_fp16.h>
 
 #include "mx4.cuh"

@@ -19,6 +19,8 @@
 // into shared memory and its heads share them; computed per value they would
 // cost more issue slots than the memory time allows (2 x ~40 instructions per
 // pair against 4 bytes moved per bf16 value pair at 44 B/ns per SM).
+// 8192 tokens x 64 heads x 128 dims, half of them rotated: 54 us, 76 % of the measured
+// copy rate; what is left is latency (each thread has one unit in flight).
 // A thread handles 16-byte vectors where base, strides, offset and rot_dim
 // allow it, else single elements (slices at odd offsets).
 #include <cuda_bf16.h>
@@ -144,12 +146,14 @@ cudaError_t launch_rope(const RopeCall& r, cudaStream_t st) {
   const bool vec = (reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.out)) % 16 == 0 && ok(r.xt) &&
                    ok(r.xh) && ok(r.ot) && ok(r.oh) && ok(r.offset) && ok(r.D) &&
                    ok(r.half_layout ? r.rot / 2 : r.rot);
-  // units of a row, and a block's share: about four units per thread when that
-  // still fills the GPU, else one (small calls are latency, not bandwidth)
+  // units of a row, and a block's share: about four units per thread where the units
+  // fill the GPU's threads, so that a block's angles serve more of them (8192 tokens x 64
+  // heads of 64 dims: 27.9 us, 36.6 with one unit), else one (64 x 128 heads: 2.1 us,
+  // 3.1 with four; 256 x 128: 3.7 and 3.5)
   const int lanes = vec ? W : 1;
   const int64_t units = (r.half_layout || !vec ? r.rot / 2 / lanes : r.rot / lanes) + (a.copy ? (r.D - r.rot) / lanes : 0);
   const int64_t all = units * r.H * r.T;
-  const int64_t want = all >= (int64_t)148 * 8 * 4 * kThreads ? 4 * kThreads : kThreads;
+  const int64_t want = all >= (int64_t)148 * 6 * kThreads ? 4 * kThreads : kThreads;
   if (units * r.H >= want) {
     a.hb = (int)((want + units - 1) / units);
   } else {
