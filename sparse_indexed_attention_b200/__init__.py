@@ -1,6 +1,7 @@
 """Python binding of libdsa (include/dsa.h): index-selected sparse attention on B200.
 
-Argument marshalling only.  Every step of the path runs in libdsa's CUDA
+Argument marshalling only (what runs on every call is native: csrc/binding.cpp).
+Every step of the path runs in libdsa's CUDA
 kernels; torch provides device memory and the current stream.  There is no
 fallback: if libdsa.so is missing and cannot be built, importing this package
 raises.
@@ -29,6 +30,7 @@ if _build.is_stale():
     _build.build_library()
 _lib = ctypes.CDLL(_build.LIB)
 LIB_PATH = _build.LIB
+from . import _binding  # noqa: E402  (linked to the library just loaded)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_BAD_INDEX, \
     DSA_ERR_TIMEOUT = range(7)
@@ -137,47 +139,15 @@ def _stream(device: torch.device):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
-def _on(device: torch.device):
-    """Makes `device` current for a launch, where another one is."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return _NOTHING
-    return torch.cuda.device(device)
-
-
-def _need(t, name: str, dtypes, shape, device: torch.device, min_rows: int = 0):
-    """Refuse, before any C call, a tensor the kernels would misread: each must
-    be a contiguous tensor on `device` with one of `dtypes`, a shape matching
-    `shape` (None matches any size) and at least `min_rows` rows.  The kernels
-    take bare pointers, so a wrong dtype, a strided view or a short pool would
-    otherwise be read out of bounds."""
-    try:  # fast path: one pass over the metadata, no message building
-        sz = t.shape
-        if t.dtype in dtypes and t.device == device and t.is_contiguous() and (sz == shape or _fits(sz, shape)) \
-                and (min_rows == 0 or sz[0] >= min_rows):
-            return
-    except (AttributeError, IndexError):
-        pass
-    _refuse(t, name, dtypes, shape, device, min_rows)
-
-
-def _fits(sz, shape) -> bool:
-    if len(sz) != len(shape):
-        return False
-    for g, w in zip(sz, shape):
-        if w is not None and g != w:
-            return False
-    return True
+# Refuses, before any C call, a tensor the kernels would misread: need(t, name,
+# dtypes, shape, device, min_rows=0) wants a contiguous tensor on `device` with
+# one of `dtypes`, a shape matching `shape` (None matches any size) and at least
+# `min_rows` rows.  The kernels take bare pointers, so a wrong dtype, a strided
+# view or a short pool would otherwise be read out of bounds.
+_need = _binding.need
+_need_seqs = _binding.need_seqs
+_cuda_device = _binding.cuda_device
+_empty = _binding.empty
 
 
 def _refuse(t, name, dtypes, shape, device, min_rows):
@@ -195,29 +165,17 @@ def _refuse(t, name, dtypes, shape, device, min_rows):
     raise ValueError(f"{name}: must be contiguous")
 
 
-def _cuda_device(t, name: str) -> torch.device:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    return t.device
-
-
 _I32T, _F32T, _BF16T = (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _FP8T, _U8T = (torch.uint8, torch.float8_e4m3fn), (torch.uint8,)
 
 
-def _need_seqs(seqs: "Seqs", dev: torch.device):
-    qs, cl, pt = seqs.q_seq_start, seqs.ctx_len, seqs.page_table
-    try:  # fast path
-        B = cl.shape[0]
-        if qs.dtype is torch.int32 and cl.dtype is torch.int32 and pt.dtype is torch.int32 and qs.shape == (B + 1,) \
-                and len(cl.shape) == 1 and pt.shape == (B, pt.shape[-1]) and qs.device == dev and cl.device == dev \
-                and pt.device == dev and qs.is_contiguous() and cl.is_contiguous() and pt.is_contiguous():
-            return
-    except (AttributeError, IndexError):
-        pass
+def _refuse_seqs(seqs, dev: torch.device):
     _need(seqs.q_seq_start, "seqs.q_seq_start", _I32T, (seqs.batch + 1,), dev)
     _need(seqs.ctx_len, "seqs.ctx_len", _I32T, (None,), dev)
     _need(seqs.page_table, "seqs.page_table", _I32T, (seqs.batch, None), dev)
+
+
+_binding.refusals(_refuse, _refuse_seqs)
 
 
 def _need_ws(ws, dev: torch.device):
@@ -228,7 +186,7 @@ def _space(ws, nbytes: int, dev: torch.device, key) -> torch.Tensor:
     """The caller's workspace, checked, or the cached one."""
     if ws is None:
         return workspace(nbytes, dev, key)
-    _need_ws(ws, dev)
+    _need(ws, "ws", _U8T, (None,), dev)
     return ws
 
 
@@ -325,6 +283,7 @@ def dsa_workspace_size(op: int, seqs: Seqs | None = None, K: int = 1, H: int = 1
 
 
 _ws_cache: dict = {}
+_ws_captured: dict = {}
 
 
 def workspace(nbytes: int, device, key=None) -> torch.Tensor:
@@ -337,18 +296,22 @@ def workspace(nbytes: int, device, key=None) -> torch.Tensor:
 
     During stream capture a buffer that is not cached yet belongs to the graph
     alone (its zeroing is part of the graph and has not run), so it is not
-    cached; a captured call whose error flag is to be read passes its own."""
+    cached; a captured call whose error flag is to be read passes its own.  A
+    cached buffer that a capture uses stays alive when a larger one replaces it:
+    the graph still writes to it."""
     if not isinstance(device, torch.device):
         device = torch.device(device)
     if device.index is None and device.type == "cuda":
         device = torch.device("cuda", torch.cuda.current_device())
     k = (device, key)
     ws = _ws_cache.get(k)
+    capturing = device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing()
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-            return ws
-        _ws_cache[k] = ws
+        if not capturing:
+            _ws_cache[k] = ws
+    elif capturing:
+        _ws_captured[ws.data_ptr()] = ws
     return ws
 
 
@@ -366,8 +329,7 @@ def dsa_quantize_index_query(qI: torch.Tensor, w: torch.Tensor, codes=None, w_sc
     _need(w, "w", _F32T, (T, 64), dev)
     _need(codes, "codes", _FP8T, (T, 64, 128), dev)
     _need(w_scaled, "w_scaled", _F32T, (T, 64), dev)
-    _check(_lib.dsa_quantize_index_query(_ptr(qI), _ptr(w), T, _ptr(codes), _ptr(w_scaled), _stream(qI.device)),
-           "dsa_quantize_index_query")
+    _check(_binding.dsa_quantize_index_query(dev, qI, w, T, codes, w_scaled), "dsa_quantize_index_query")
     return codes, w_scaled
 
 
@@ -379,8 +341,7 @@ def dsa_quantize_index_query_mx(qI: torch.Tensor, codes=None, scales=None):
     _need(qI, "qI", _BF16T, (T, 64, 128), dev)
     _need(codes, "codes", _FP8T, (T, 64, 128), dev)
     _need(scales, "scales", (torch.uint8,), (T, 64, 4), dev)
-    _check(_lib.dsa_quantize_index_query_mx(_ptr(qI), T, _ptr(codes), _ptr(scales), _stream(qI.device)),
-           "dsa_quantize_index_query_mx")
+    _check(_binding.dsa_quantize_index_query_mx(dev, qI, T, codes, scales), "dsa_quantize_index_query_mx")
     return codes, scales
 
 
@@ -391,16 +352,14 @@ def dsa_quantize_index_query_mx4(qI: torch.Tensor, codes=None, scales=None):
     _need(qI, "qI", _BF16T, (qI.shape[0], 64, 128), dev)
     T = qI.shape[0]
     if codes is None:
-        codes = qI.new_empty((T, 64, 64), dtype=torch.uint8)
+        codes = _empty((T, 64, 64), torch.uint8, dev)
     else:
         _need(codes, "codes", _U8T, (T, 64, 64), dev)
     if scales is None:
-        scales = qI.new_empty((T, 64, 4), dtype=torch.uint8)
+        scales = _empty((T, 64, 4), torch.uint8, dev)
     else:
         _need(scales, "scales", _U8T, (T, 64, 4), dev)
-    with _on(dev):
-        _check(_lib.dsa_quantize_index_query_mx4(_ptr(qI), T, _ptr(codes), _ptr(scales), _stream(dev)),
-               "dsa_quantize_index_query_mx4")
+    _check(_binding.dsa_quantize_index_query_mx4(dev, qI, T, codes, scales), "dsa_quantize_index_query_mx4")
     return codes, scales
 
 
@@ -413,11 +372,9 @@ def dsa_append_index_keys_mx4(seqs: Seqs, k: torch.Tensor, kI: torch.Tensor, kI_
     rows = seqs.num_phys_pages * 64
     _need(kI, "kI", _U8T, (None, 64), dev, rows)
     _need(kI_scale, "kI_scale", _U8T, (None, 4), dev, rows)
-    c = seqs.c()
     ws = _space(ws, 256, dev, "append_index_keys")
-    with _on(dev):
-        _check(_lib.dsa_append_index_keys_mx4(ctypes.byref(c), _ptr(k), _ptr(kI), _ptr(kI_scale), _ptr(ws),
-                                              ws.numel(), _stream(dev)), "dsa_append_index_keys_mx4")
+    _check(_binding.dsa_append_index_keys_mx4(dev, seqs, k, kI, kI_scale, ws, ws.numel()),
+           "dsa_append_index_keys_mx4")
 
 
 def dsa_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None) -> torch.Tensor:
@@ -430,12 +387,10 @@ def dsa_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out=None) -> t
     _need(codes, "codes", _U8T, codes.shape, dev)
     _need(scales, "scales", _U8T, (*lead, 4), dev)
     if out is None:
-        out = codes.new_empty((*lead, 128), dtype=torch.bfloat16)
+        out = _empty((*lead, 128), torch.bfloat16, dev)
     else:
         _need(out, "out", _BF16T, (*lead, 128), dev)
-    with _on(dev):
-        _check(_lib.dsa_dequantize_mx4(_ptr(codes), _ptr(scales), codes.numel() // 64, _ptr(out), _stream(dev)),
-               "dsa_dequantize_mx4")
+    _check(_binding.dsa_dequantize_mx4(dev, codes, scales, codes.numel() // 64, out), "dsa_dequantize_mx4")
     return out
 
 
@@ -455,12 +410,9 @@ def dsa_index_scores(seqs: Seqs, qI, w, kI, kI_scale=None, scores=None, ld=None,
             raise ValueError(f"ld={ld} differs from the row stride {scores.stride(0)} of scores")
         ld = scores.stride(0)
     ki_dtype = _ki_dtype(kI_scale, kI)
-    c = seqs.c()
-    need = _lib.dsa_workspace_size(DSA_OP_INDEX_SCORES, ctypes.byref(c), 1, 16)
-    ws = _space(ws, need, dev, "index_scores")
-    with _on(dev):
-        _check(_lib.dsa_index_scores(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype,
-                                     _ptr(scores), ld, _ptr(ws), ws.numel(), _stream(dev)), "dsa_index_scores")
+    ws = _space(ws, _binding.workspace_size(DSA_OP_INDEX_SCORES, seqs, 1, 16), dev, "index_scores")
+    _check(_binding.dsa_index_scores(dev, seqs, qI, w, kI, kI_scale, ki_dtype, scores, ld, ws, ws.numel()),
+           "dsa_index_scores")
     return scores
 
 
@@ -477,8 +429,7 @@ def dsa_topk(scores: torch.Tensor, row_len: torch.Tensor, K: int, idx=None, ws=N
     need = _lib.dsa_workspace_size(DSA_OP_TOPK, ctypes.byref(c), K, 16)
     ws = ws if ws is not None else workspace(need, scores.device, "topk")
     _need_ws(ws, dev)
-    _check(_lib.dsa_topk(_ptr(scores), ld, T, _ptr(row_len), K, _ptr(idx), _ptr(ws), ws.numel(),
-                         _stream(scores.device)), "dsa_topk")
+    _check(_binding.dsa_topk(dev, scores, ld, T, row_len, K, idx, ws, ws.numel()), "dsa_topk")
     return idx
 
 
@@ -501,14 +452,12 @@ def dsa_sparse_mla_fwd(seqs: Seqs, q, kv, idx, scale: float, out=None, lse=None,
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     dev = _need_attn_inputs(seqs, q, kv, out, lse, kv_scale)
     _need(idx, "idx", _I32T, (T, K), dev)
-    c = seqs.c()
-    need = _lib.dsa_workspace_size(DSA_OP_SPARSE_MLA, ctypes.byref(c), K, H)
+    need = _binding.workspace_size(DSA_OP_SPARSE_MLA, seqs, K, H)
     ws = ws if ws is not None else workspace(need, q.device, "sparse_mla")
     _need_ws(ws, dev)
     kv_dtype = DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3
-    _check(_lib.dsa_sparse_mla_fwd_ex(ctypes.byref(c), _ptr(q), _ptr(kv), _ptr(kv_scale), kv_dtype, _ptr(idx), K, H,
-                                      scale, _ptr(out), _out_dtype(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                      _stream(q.device)), "dsa_sparse_mla_fwd")
+    _check(_binding.dsa_sparse_mla_fwd_ex(dev, seqs, q, kv, kv_scale, kv_dtype, idx, K, H, scale, out,
+                                          _out_dtype(out), lse, ws, ws.numel()), "dsa_sparse_mla_fwd")
     return out, lse
 
 
@@ -524,9 +473,7 @@ def dsa_sparse_mla_fwd_noalloc(seqs: Seqs, q, kv, idx, scale: float, out=None, l
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     dev = _need_attn_inputs(seqs, q, kv, out, lse)
     _need(idx, "idx", _I32T, (T, K), dev)
-    c = seqs.c()
-    _check(_lib.dsa_sparse_mla_fwd_noalloc(ctypes.byref(c), _ptr(q), _ptr(kv), _ptr(idx), K, H, scale, _ptr(out),
-                                           _out_dtype(out), _ptr(lse), _stream(q.device)),
+    _check(_binding.dsa_sparse_mla_fwd_noalloc(dev, seqs, q, kv, idx, K, H, scale, out, _out_dtype(out), lse),
            "dsa_sparse_mla_fwd_noalloc")
     return out, lse
 
@@ -549,19 +496,16 @@ def dsa_index_topk_attn(seqs: Seqs, qI, w, kI, kI_scale, q, kv, K: int, scale: f
     if idx_out is not None:
         _need(idx_out, "idx_out", _I32T, (T, K), dev)
     ki_dtype = _ki_dtype(kI_scale, kI)
-    c = seqs.c()
     op = DSA_OP_INDEX_TOPK_ATTN_FUSED if select_in_indexer else DSA_OP_INDEX_TOPK_ATTN
-    need = _lib.dsa_workspace_size(op, ctypes.byref(c), K, H)
+    need = _binding.workspace_size(op, seqs, K, H)
     ws = ws if ws is not None else workspace(need, q.device, "index_topk_attn")
     _need_ws(ws, dev)
-    ev = None if q_ready is None else ctypes.c_void_p(q_ready.cuda_event)
+    ev = None if q_ready is None else q_ready.cuda_event
     kv_dtype = DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3
-    with _on(dev):
-        _check(_lib.dsa_index_topk_attn_ex(ctypes.byref(c), _ptr(qI), _ptr(w), _ptr(kI), _ptr(kI_scale), ki_dtype,
-                                           _ptr(q), _ptr(kv), _ptr(kv_scale), kv_dtype, K, H, scale, _ptr(out),
-                                           _out_dtype(out), _ptr(lse), _ptr(idx_out), _ptr(ws), ws.numel(),
-                                           DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev, _stream(dev)),
-               "dsa_index_topk_attn")
+    _check(_binding.dsa_index_topk_attn_ex(dev, seqs, qI, w, kI, kI_scale, ki_dtype, q, kv, kv_scale, kv_dtype, K, H,
+                                           scale, out, _out_dtype(out), lse, idx_out, ws, ws.numel(),
+                                           DSA_SELECT_IN_INDEXER if select_in_indexer else 0, ev),
+           "dsa_index_topk_attn")
     return out, lse
 
 
@@ -588,13 +532,9 @@ def dsa_attn_mass(seqs: Seqs, q, kv, idx, lse, scale: float, mass, kv_scale=None
     _need(mass, "mass", _I64T, (seqs.batch, None), dev)
     if mass.shape[1] < seqs.max_ctx:
         raise ValueError(f"mass: {mass.shape[1]} positions per sequence, max_ctx is {seqs.max_ctx}")
-    c = seqs.c()
     ws = _space(ws, 256, dev, "attn_mass")
-    with _on(dev):
-        _check(_lib.dsa_attn_mass(ctypes.byref(c), q.data_ptr(), kv.data_ptr(), _ptr(kv_scale),
-                                  DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3, idx.data_ptr(), idx.shape[1],
-                                  H, scale, lse.data_ptr(), mass.data_ptr(), mass.shape[1], ws.data_ptr(), ws.numel(),
-                                  _stream(dev)), "dsa_attn_mass")
+    _check(_binding.dsa_attn_mass(dev, seqs, q, kv, kv_scale, DSA_KV_BF16 if kv_scale is None else DSA_KV_FP8_E4M3, idx,
+                                  idx.shape[1], H, scale, lse, mass, mass.shape[1], ws, ws.numel()), "dsa_attn_mass")
     return mass
 
 
@@ -610,18 +550,16 @@ def dsa_evict_select(ctx_len, mass, budget: int, recent: int = 0, sink: int = 0,
     if budget < 1 or recent < 0 or sink < 0 or recent + sink > budget:
         raise ValueError(f"budget={budget}, recent={recent}, sink={sink}: expected recent + sink <= budget, budget >= 1")
     if keep is None:
-        keep = mass.new_empty((B, budget), dtype=torch.int32)
+        keep = _empty((B, budget), torch.int32, dev)
     else:
         _need(keep, "keep", _I32T, (B, budget), dev)
     if keep_len is None:
-        keep_len = mass.new_empty((B,), dtype=torch.int32)
+        keep_len = _empty((B,), torch.int32, dev)
     else:
         _need(keep_len, "keep_len", _I32T, (B,), dev)
     ws = _space(ws, 256, dev, "evict_select")
-    with _on(dev):
-        _check(_lib.dsa_evict_select(ctx_len.data_ptr(), B, ld, mass.data_ptr(), ld, budget, recent, sink,
-                                     keep.data_ptr(), keep_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
-               "dsa_evict_select")
+    _check(_binding.dsa_evict_select(dev, ctx_len, B, ld, mass, ld, budget, recent, sink, keep, keep_len, ws, ws.numel()),
+           "dsa_evict_select")
     return keep, keep_len
 
 
@@ -637,69 +575,63 @@ def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=No
     _need(keep, "keep", _I32T, (B, None), dev)
     _need(keep_len, "keep_len", _I32T, (B,), dev)
     _need(new_page_table, "new_page_table", _I32T, (B, None), dev)
-    n = len(pools)
-    if n > DSA_MAX_POOLS:
-        raise ValueError(f"{n} pools, at most {DSA_MAX_POOLS}")
-    cp = (DsaPoolC * max(n, 1))()
-    pages = seqs.num_phys_pages
-    new_pages = None
-    for i, p in enumerate(pools):
-        src, dst = p if isinstance(p, (tuple, list)) else (p, p)
-        for t in (src,) if dst is src else (src, dst):
-            if not isinstance(t, torch.Tensor) or t.dim() < 1:
-                raise TypeError(f"pools[{i}]: expected a tensor of rows")
-        n_src = src.shape[0]
-        if n_src < pages * 64 or not src.is_contiguous() or src.device != dev:
-            _need(src, f"pools[{i}]", (src.dtype,), tuple(src.shape), dev, pages * 64)
-        here = pages
-        if dst is not src:
-            _need(dst, f"pools[{i}] destination", (src.dtype,), (dst.shape[0], *src.shape[1:]), dev, 64)
-            here = dst.shape[0] // 64
-        new_pages = here if new_pages is None else min(new_pages, here)
-        c_pool = cp[i]
-        c_pool.src, c_pool.dst = src.data_ptr(), dst.data_ptr()
-        c_pool.row_bytes = src.stride(0) * src.element_size()
-    new_pages = pages if new_pages is None else new_pages
+    packed = _binding.pools(pools, seqs.num_phys_pages, dev)
+    if packed is None:
+        _refuse_pools(pools, seqs.num_phys_pages, dev)
+    c_pools, new_pages = packed
     ld = new_ld = 0
     if mass is not None or new_mass is not None:
         _need(mass, "mass", _I64T, (B, None), dev)
         _need(new_mass, "new_mass", _I64T, (B, None), dev)
         ld, new_ld = mass.shape[1], new_mass.shape[1]
-    c = seqs.c()
     need = 256 + (3 * ((new_pages + 31) // 32) * 4 + 255) // 256 * 256
     # one cached buffer per size: a captured call's buffer is never replaced by a larger one
     ws = _space(ws, need, dev, ("evict_compact", need))
-    with _on(dev):
-        _check(_lib.dsa_evict_compact(ctypes.byref(c), keep.data_ptr(), keep_len.data_ptr(), keep.shape[1],
-                                      new_page_table.data_ptr(), new_page_table.shape[1], new_pages, cp, n, _ptr(mass),
-                                      ld, _ptr(new_mass), new_ld, ws.data_ptr(), ws.numel(), _stream(dev)),
-               "dsa_evict_compact")
+    _check(_binding.dsa_evict_compact(dev, seqs, keep, keep_len, keep.shape[1], new_page_table, new_page_table.shape[1],
+                                      new_pages, c_pools, len(pools), mass, ld, new_mass, new_ld, ws, ws.numel()),
+           "dsa_evict_compact")
+
+
+def _refuse_pools(pools, pages: int, dev: torch.device):
+    if len(pools) > DSA_MAX_POOLS:
+        raise ValueError(f"{len(pools)} pools, at most {DSA_MAX_POOLS}")
+    for i, p in enumerate(pools):
+        src, dst = p if isinstance(p, (tuple, list)) else (p, p)
+        for t in (src, dst):
+            if not isinstance(t, torch.Tensor) or t.dim() < 1:
+                raise TypeError(f"pools[{i}]: expected a tensor of rows")
+        _need(src, f"pools[{i}]", (src.dtype,), tuple(src.shape), dev, pages * 64)
+        if dst is not src:
+            _need(dst, f"pools[{i}] destination", (src.dtype,), (dst.shape[0], *src.shape[1:]), dev, 64)
+    raise ValueError("pools: expected a list of tensors or pairs of tensors whose rows have less than 2^31 bytes")
 
 
 _ROPE_DTYPES = {torch.bfloat16: DSA_ROPE_BF16, torch.float16: DSA_ROPE_F16, torch.float32: DSA_ROPE_F32}
 
 
+_POS_T = (torch.int64, torch.int32)
+
+
 def _rope_view(t, name: str, dev: torch.device, dtype):
     """[T, H, D] sizes and [T, H] strides of a [T, H, D] or [T, D] tensor
     whose last dim is contiguous (the stride of a dim of one entry is 0)."""
+    return _binding.rows(t, dtype, dev) or _refuse_rows(t, name, dev, dtype)
+
+
+def _refuse_rows(t, name: str, dev: torch.device, dtype):
+    """Says why t is no [T, H, D] or [T, D] tensor with a contiguous last dim."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    sz, st = t.shape, t.stride()
-    if len(sz) == 2:
-        T, H, D, a, b, last = sz[0], 1, sz[1], st[0], 0, st[1]
-    elif len(sz) == 3:
-        (T, H, D), (a, b, last) = sz, st
-    else:
+    sz = t.shape
+    if len(sz) not in (2, 3):
         raise ValueError(f"{name}: shape {list(sz)}, expected [T, H, D] or [T, D]")
-    if H < 1 or D < 1:
+    if 0 in sz[1:]:
         raise ValueError(f"{name}: shape {list(sz)} has no heads or no dims")
-    if last != 1 and D > 1:
-        raise ValueError(f"{name}: the last dim must be contiguous")
-    return T, H, D, a if T > 1 else 0, b if H > 1 else 0
+    raise ValueError(f"{name}: the last dim must be contiguous")
 
 
 def _rope_disjoint(x, out, T, H, D, xt, xh, ot, oh) -> bool:
@@ -729,37 +661,36 @@ def dsa_rope(x: torch.Tensor, positions: torch.Tensor, table: RopeTable, offset:
     that of x (with amplitude 1 it undoes the rotation).  The call records no
     autograd graph and refuses an x that would need one."""
     dev = _cuda_device(x, "x")
-    kind = _ROPE_DTYPES.get(x.dtype)
+    dtype = x.dtype
+    kind = _ROPE_DTYPES.get(dtype)
     if kind is None:
-        raise TypeError(f"x: dtype {x.dtype}, expected one of {[str(d) for d in _ROPE_DTYPES]}")
+        raise TypeError(f"x: dtype {dtype}, expected one of {[str(d) for d in _ROPE_DTYPES]}")
     if x.requires_grad and torch.is_grad_enabled():
         raise RuntimeError("dsa_rope records no gradients: call it under torch.no_grad() and rotate the output's "
                            "gradient with transpose=True")
-    T, H, D, xt, xh = _rope_view(x, "x", dev, x.dtype)
+    T, H, D, xt, xh = _rope_view(x, "x", dev, dtype)
     if not isinstance(table, RopeTable):
         raise TypeError(f"table: expected a RopeTable, got {type(table).__name__}")
-    _need(table.turns, "table.turns", (torch.int64,), (table.rot_dim // 2,), dev)
-    _need(positions, "positions", (torch.int64, torch.int32), (T,), dev)
+    turns, rot_dim = table.turns, table.rot_dim
+    _need(turns, "table.turns", _I64T, (rot_dim // 2,), dev)
+    _need(positions, "positions", _POS_T, (T,), dev)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _empty(tuple(x.shape), dtype, dev)
         ot, oh = H * D if T > 1 else 0, D if H > 1 else 0
+    elif out is x:
+        ot, oh = xt, xh
     else:
-        if out is x:
-            ot, oh = xt, xh
-        else:
-            ot, oh = _rope_view(out, "out", dev, x.dtype)[3:]
-            if out.shape != x.shape:
-                raise ValueError(f"out: shape {list(out.shape)}, expected {list(x.shape)}")
-            if out.requires_grad and torch.is_grad_enabled():
-                raise RuntimeError("out: dsa_rope records no gradients")
+        ot, oh = _rope_view(out, "out", dev, dtype)[3:]
+        if out.shape != x.shape:
+            raise ValueError(f"out: shape {list(out.shape)}, expected {list(x.shape)}")
+        if out.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("out: dsa_rope records no gradients")
         if T and not _rope_disjoint(x, out, T, H, D, xt, xh, ot, oh):
             raise ValueError("x and out overlap without being the same view")
     flags = (0 if table.interleaved else DSA_ROPE_HALF) | (DSA_ROPE_TRANSPOSE if transpose else 0) \
-        | (DSA_ROPE_POS64 if positions.dtype == torch.int64 else 0)
-    with _on(dev):
-        _check(_lib.dsa_rope(x.data_ptr(), out.data_ptr(), kind, T, H, D, xt, xh, ot, oh, positions.data_ptr(),
-                             table.turns.data_ptr(), table.rot_dim, offset, table.amplitude, flags, _stream(dev)),
-               "dsa_rope")
+        | (DSA_ROPE_POS64 if positions.dtype is torch.int64 else 0)
+    _check(_binding.dsa_rope(dev, x, out, kind, T, H, D, xt, xh, ot, oh, positions, turns, rot_dim, offset,
+                             table.amplitude, flags), "dsa_rope")
     return out
 
 

@@ -1,4 +1,5 @@
-"""Builds libdsa.so in-tree with nvcc for sm_100a (no GPU needed to build).
+"""Builds libdsa.so (nvcc, sm_100a) and the Python binding's native part
+_binding.so (g++, on torch's headers) in-tree.  No GPU needed to build.
 
     python -m sparse_indexed_attention_b200.build [--force]
 """
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -37,13 +40,13 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [
-        os.path.abspath(__file__)]
+        BINDING_SRC, os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
@@ -56,6 +59,23 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         if not force and not is_stale():
             return LIB
         return _build(verbose)
+
+
+def _binding_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: _binding.so cannot be built")
+    inc = [os.path.join(t, "include"), os.path.join(t, "include/torch/csrc/api/include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    return [cxx, "-O2", "-fPIC", "-shared", "-std=c++17", *(a for d in inc for a in ("-isystem", d)), BINDING_SRC, "-o",
+            out, "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L", PKG, "-l:libdsa.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def _build(verbose: bool) -> str:
@@ -79,6 +99,11 @@ def _build(verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
