@@ -30,13 +30,14 @@
 //    (two MMAs of 64 dims per tile): half the bytes of a key and twice the tensor
 //    rate.  A page is loaded as 32 rows of two keys, and a stage holds 256 keys: its
 //    even keys are the first halves of 128 rows in the 128-byte swizzle, its odd keys
-//    the second halves, each the A operand of a tile (half the steps per key: 8 x
-//    131,072 keys 27.8 -> 26.5 us, 2 x 1000 queries at 8 K 211 -> 200 us).  What is left
-//    above the 71 MB of the decode call (11 us at the measured copy rate) is the start,
-//    4.5 us until the plan is there and the first stage has landed, and the epilogue;
-//    prefill is bound by the epilogue, 64 products and maxima per score.
+//    the second halves, each the A operand of a tile (half the steps per key).
+//    8 x 131,072 keys take 24.7 us: 71 MB (11 us at the measured copy rate), 4.5 us
+//    until the plan is there and the first stage has landed, and pages that arrive at
+//    3.5 TB/s (22 us without the epilogue's products).  1000-token prompts at 8 K take
+//    174 us, bound by the epilogue's 64 maxima per score (ALU pipe 59 % busy; 113 us
+//    without maxima and products).
 //  * warp 2: allocates and frees TMEM (MXFP4: also issues each stage's second tile).
-//  * warps 4-11 (MXFP4: 4-19): epilogue, two (four) warpgroups sharing the tiles.  Thread r
+//  * warps 4-11: epilogue, two warpgroups sharing the tiles.  Thread r
 //    of a warpgroup owns TMEM lane r = key row r, so the ReLU, the head
 //    weighting and the reduction over heads stay inside one thread; no
 //    [T, H_I, N] value ever leaves the SM.
@@ -112,27 +113,38 @@ struct IdxCfg {
   // barrier's parity tells the next phase from this one only).  MXFP4, 8 x 131,072
   // keys: 36.4 us with one, 29.6 with two.
   static constexpr int NPROD = NS % 2 == 0 && !kFused ? 2 : 1;
-  // Epilogue warpgroups (from warp 4).  MXFP4 tiles come twice as fast, so four
-  // warpgroups share them: with one token per group each takes every fourth tile, with
-  // two each takes one token of every other tile (decode 29.6 -> 27.8 us, prefill
-  // 223 -> 211 us).
-  static constexpr int NWG = kMx4 && !kFused ? 4 : 2;
+  // Two epilogue warpgroups (from warp 4).  With MXFP4's two tokens per group each
+  // takes one token of every tile, else each every other tile: an MXFP4 thread then
+  // needs one token's 64 weights, and keeps them in registers.  Four warpgroups must
+  // read them from shared memory, 16 bytes a lane for every four products (8 x
+  // 131,072 keys 26.1 us against 24.7, 1000-token prompts 200 against 187); four that
+  // split the heads in two pay more for handing over the sums (29.6 and 260).
+  static constexpr int NWG = 2;
   static constexpr int EPI = 4 * NWG;                      // warps
   static constexpr int THREADS = (4 + EPI) * 32;
-  static constexpr int TILE_WGS = TG == 1 ? NWG : 2;       // tile i -> the warpgroups that are i mod TILE_WGS
+  static constexpr int TILE_WGS = kMx4 && TG == 2 ? 1 : 2;  // tile i -> the warpgroups that are i mod TILE_WGS
   static constexpr int TOKEN_WGS = NWG / TILE_WGS;         // which then take the group's tokens in turn
+  static constexpr bool PIPED = kMx4;                      // see the epilogue
+  // How the CTAs share the work items: a prompt's groups end in items of one to eight
+  // tiles, and contiguous runs of equally many items left the slowest SM with 16 %
+  // more than the mean (1000-token prompts 187 -> 174 us).
+  static constexpr bool SPREAD = kMx4 && TG > 1;
   // MMA issuers: one per tile of a stage (warp 2, which owns TMEM, issues the
   // second one's), since the waits, copies and commits around a tile's MMAs are one chain.
   static constexpr int NISS = SUB;
-  // Accumulator ring.  NACC is even: the two epilogue warpgroups take
-  // alternate tiles, so each accumulator (and its barriers) belongs to one
-  // warpgroup and is waited on one phase at a time.  MXFP8 also keeps scale
-  // columns in TMEM: 4 per stage (128 keys), 4 per group slot and 128 query rows.
-  static constexpr int NACC = kMx ? (N == 64 ? 4 : 2) : ((512 / N) < 4 ? (512 / N) : 4);
+  // Accumulator ring.  NACC is even where the two epilogue warpgroups take
+  // alternate tiles, so that each accumulator (and its barriers) belongs to one
+  // warpgroup and is waited on one phase at a time.  Where both take every tile
+  // (TILE_WGS = 1) three will do: each warp releases the tiles in order, so an issuer
+  // that saw tile i - 5 released (for its tile i - 2) knows that i - 6 was, and
+  // its wait for i - 3 cannot mistake the one for the other.  The MX caches
+  // also keep scale columns in TMEM: 4 per accumulator, free again with it, and 4 per
+  // group slot and 128 query rows.
+  static constexpr int NACC = kMx4 ? (N == 64 ? 6 : 3) : kMx ? (N == 64 ? 4 : 2) : ((512 / N) < 4 ? (512 / N) : 4);
   static constexpr int SFB_COPIES = kMx ? (N + 127) / 128 : 0;   // 32x128b copies per group
   static constexpr int SFB_BYTES = SFB_COPIES * 512;
-  static constexpr int SFA0 = NACC * N;                    // TMEM column of stage 0's key scales
-  static constexpr int SFB0 = SFA0 + 4 * SUB * NS;               // TMEM column of slot 0's query scales
+  static constexpr int SFA0 = NACC * N;                    // TMEM column of accumulator 0's key scales
+  static constexpr int SFB0 = SFA0 + 4 * NACC;             // TMEM column of slot 0's query scales
   static constexpr int SFB_COLS = 4 * SFB_COPIES;
   static constexpr int TMEM_COLS = kMx ? 512 : ((NACC * N) <= 256 ? 256 : 512);
   // shared-memory layout (offsets from a 1024-aligned base)
@@ -157,7 +169,7 @@ struct IdxCfg {
   static constexpr uint32_t IDESC = make_idesc(kBf16, 128, N);
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NACC * N <= TMEM_COLS && NACC % TILE_WGS == 0, "each TMEM accumulator belongs to its warpgroups");
-  static_assert(NACC % NISS == 0, "and to its issuer");
+  static_assert(NACC % NISS == 0 || TILE_WGS == 1, "and to its issuer");
   static_assert(!kMx || SFB0 + 2 * NISS * SFB_COLS <= TMEM_COLS, "TMEM scale columns");
   static_assert(OFF_SFB % 512 == 0, "scale-factor sources need 16-byte alignment");
   static_assert(!kFused || CAP_ITEMS >= 8, "fused selection capacity");
@@ -548,6 +560,18 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
+// sum over 32 heads of w relu(v): two products per instruction, four chains.
+__device__ __forceinline__ float weigh32(const uint32_t (&v)[32], const float* w) {
+  uint64_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int h = 0; h < 32; h += 2)
+    c[h / 2 % 4] = fma2(w[h], w[h + 1], relu(v[h]), relu(v[h + 1]), c[h / 2 % 4]);
+  float p[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(c[i], p[2 * i], p[2 * i + 1]);
+  return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+}
+
 // Adds one epilogue warp's histogram of the current token to the global one
 // and clears it (warp-private, so only the warp synchronises).
 __device__ __forceinline__ void flush_hist(uint32_t* sh, uint32_t* gh, int t, int lane) {
@@ -612,10 +636,15 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   pdl_wait();  // the plan and the quantized query come from the previous kernel
   pdl_trigger();
 
-  // this CTA's contiguous share of the work items
+  // this CTA's share of the work items: a contiguous run, or (SPREAD) one item of
+  // every gridDim.x, a place further each time so that the share does not fall
+  // on the short last items of the groups or miss them
   const int n_items = a.plan.counts[1];
-  const int it_lo = (int)(((int64_t)n_items * blockIdx.x) / gridDim.x);
-  const int it_hi = (int)(((int64_t)n_items * (blockIdx.x + 1)) / gridDim.x);
+  const int grid = (int)gridDim.x, bx = (int)blockIdx.x, rounds = n_items / grid;
+  const int it_lo = C::SPREAD ? 0 : (int)(((int64_t)n_items * bx) / grid);
+  const int it_hi = C::SPREAD ? rounds + ((bx + rounds) % grid < n_items % grid ? 1 : 0)
+                              : (int)(((int64_t)n_items * (bx + 1)) / grid);
+  auto rec_of = [&](int it) { return C::SPREAD ? it * grid + (bx + it) % grid : it; };
 
   const int4* recs = a.plan.items;  // item i: recs[2i] = {b, t0, cnt, pos0}, recs[2i+1] = {tile_begin, tile_end, g, 0}
 
@@ -635,7 +664,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     int4* ring_rec = reinterpret_cast<int4*>(ring);                     // [slot][2]
     int* ring_pg = reinterpret_cast<int*>(ring + kRingSlots * 32);     // [slot][32]
     auto issue_rec = [&](int it) {
-      if (it < it_hi && lane < 2) cp_async_16(&ring_rec[(it % kRingSlots) * 2 + lane], recs + 2 * it + lane);
+      if (it < it_hi && lane < 2) cp_async_16(&ring_rec[(it % kRingSlots) * 2 + lane], recs + 2 * rec_of(it) + lane);
     };
     auto issue_pages = [&](int it) {  // the item's record is already in the ring
       if (it >= it_hi) return;
@@ -794,10 +823,10 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       // operands stay uniform, which the issue of an MMA wants.
       const int p = C::NISS == 2 ? __shfl_sync(0xffffffffu, warp, 0) - 1 : 0;  // this issuer's tile of each stage
       int stage = 0, sphase = 0, acc = p, aphase = 0, prev_g = -1, gcount = 0, slot = 0;
-      int4 nb = it_lo < it_hi ? recs[2 * it_lo + 1] : make_int4(0, 0, 0, 0);
+      int4 nb = it_lo < it_hi ? recs[2 * rec_of(it_lo) + 1] : make_int4(0, 0, 0, 0);
       for (int it = it_lo; it < it_hi && !*abort_flag; ++it) {
         const int4 item = make_int4(nb.z, nb.x, nb.y, 0);  // {g, tile_begin, tile_end}
-        if (it + 1 < it_hi) nb = recs[2 * it + 3];
+        if (it + 1 < it_hi) nb = recs[2 * rec_of(it + 1) + 1];
         if (item.x != prev_g) {
           if (prev_g >= 0 && elect_one()) mma_commit(&b_empty[slot]);  // previous group's operands free once its MMAs finish
           slot = gcount & 1;
@@ -835,7 +864,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             if constexpr (kMx) {
               // the tile's key scales into TMEM, then one block-scaled MMA per 64
               // (MXFP4) or 32 dims, taking 2 or 1 bytes of each scale column
-              const uint32_t sfa = tmem + C::SFA0 + 4 * (C::SUB * stage + p);
+              const uint32_t sfa = tmem + C::SFA0 + 4 * acc;
               tmem_cp_32x128b_x4(sfa, rows16_desc(smem_u32(smem + C::OFF_SC + (C::SUB * stage + p) * 512)));
               if constexpr (kMx4) {
 #pragma unroll
@@ -880,14 +909,15 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     // Two warpgroups take alternate tiles (tile i -> warpgroup i & 1, which
-    // therefore owns every other TMEM accumulator; four share them for the
-    // MXFP4 cache, see NWG); all follow every group.
+    // therefore owns every other TMEM accumulator) or one token each of every
+    // tile (see NWG); both follow every group.
     const int q = (warp - 4) & 3;      // TMEM lane quarter of this warp
     const int wg = (warp - 4) >> 2;    // epilogue warpgroup
     const int r = q * 32 + lane;       // key row of the tile
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
     int stage = 0, sphase = 0, acc = 0, aphase = 0, prev_g = -1, gcount = 0, slot = 0, prev_t = -1, ti = 0;
-    float wreg[C::NWG == 2 && TG == 1 ? 64 : 1];  // (more warpgroups leave no registers for the weights)
+    constexpr bool kWReg = TG == 1 || C::PIPED;  // one token's weights
+    float wreg[kWReg ? 64 : 1];
     uint32_t* sh_hist = reinterpret_cast<uint32_t*>(smem + C::OFF_HIST) + (warp - 4) * kTopkHistBins;
     const bool do_hist = TG == 1 && !kFused && a.hist != nullptr;
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem + C::OFF_KEYS);
@@ -895,13 +925,44 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       for (int i = lane; i < kTopkHistBins; i += 32) sh_hist[i] = 0u;
       __syncwarp();
     }
+    // where key s's score for the group's token k goes, or -1
+    auto place = [&](int s, int k, const int4& grp, int it, int item_tile) -> int64_t {
+      // the host sizes the grid so that a CTA's items fit; the guard keeps
+      // an oversized share from writing past the buffer all the same
+      if constexpr (kFused) return it - it_lo < C::CAP_ITEMS ? (it - it_lo) * 1024 + s - item_tile * 128 : -1;
+      return k < grp.z && s <= grp.w + k ? (int64_t)(grp.y + k) * a.ld + s : -1;
+    };
+    auto put = [&](float score, int64_t at) {
+      if (at < 0) return;
+      if constexpr (kFused) {
+        keys[at] = order_key(score);
+      } else {
+        a.scores[at] = score;
+        // scores fall in random bins: a plain shared-memory add beats aggregating equal bins
+        if (do_hist) atomicAdd(&sh_hist[order_key(score) >> kTopkLowBits], 1u);
+      }
+    };
+    // PIPED: a tile's second half of the heads (vb) is summed behind the next tile's
+    // first load, so that a thread always has a TMEM load in flight while it
+    // multiplies; until then the tile is pending, with its first half's sum.
+    uint32_t vb[C::PIPED ? 32 : 1];
+    float pend_sum = 0.f;
+    int64_t pend_at = -1;
+    bool pending = false;
+    auto finish = [&] {
+      if constexpr (C::PIPED) {
+        if (pending) put(pend_sum + weigh32(vb, wreg + 32), pend_at);
+        pending = false;
+      }
+    };
     int4 na = make_int4(0, 0, 0, 0), nb = na;
-    if (it_lo < it_hi) { na = recs[2 * it_lo]; nb = recs[2 * it_lo + 1]; }
+    if (it_lo < it_hi) { na = recs[2 * rec_of(it_lo)]; nb = recs[2 * rec_of(it_lo) + 1]; }
     for (int it = it_lo; it < it_hi && !*abort_flag; ++it) {
       const int4 grp = na;                                // {b, t0, cnt, pos0}
       const int4 item = make_int4(nb.z, nb.x, nb.y, 0);  // {g, tile_begin, tile_end}
-      if (it + 1 < it_hi) { na = recs[2 * it + 2]; nb = recs[2 * it + 3]; }
+      if (it + 1 < it_hi) { na = recs[2 * rec_of(it + 1)]; nb = recs[2 * rec_of(it + 1) + 1]; }
       if (item.x != prev_g) {
+        finish();
         if (prev_g >= 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&b_empty[slot]);
@@ -913,9 +974,10 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           *abort_flag = 1;
           break;
         }
-        if constexpr (C::NWG == 2 && TG == 1) {
+        if constexpr (kWReg) {
+          const float* wt = w_smem + (slot * TG + (TG > 1 ? wg : 0)) * 64;
 #pragma unroll
-          for (int h = 0; h < 64; ++h) wreg[h] = w_smem[slot * TG * 64 + h];
+          for (int h = 0; h < 64; ++h) wreg[h] = wt[h];
         }
         prev_g = item.x;
         ++gcount;
@@ -935,34 +997,35 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           }
           // MXFP4: the stage's even keys, then its odd ones
           const int s = kMx4 ? (tile & ~1) * 128 + 2 * r + (tile & 1) : tile * 128 + r;
+          if constexpr (C::PIPED) {
+            const int k = TG > 1 ? wg : 0;
+            uint32_t va[32];
+            tmem_ld32(t_lane + acc * C::N + k * 64, va);
+            finish();
+            tmem_ld_wait_regs(va);
+            tmem_ld32(t_lane + acc * C::N + k * 64 + 32, vb);
+            pend_sum = weigh32(va, wreg);
+            pend_at = place(s, k, grp, it, item.y);
+            pending = true;
+            tmem_ld_wait_regs(vb);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[acc]);
+          } else {
 #pragma unroll 1
-          for (int k = wg / C::TILE_WGS; k < TG; k += C::TOKEN_WGS) {
-            uint32_t v0[32], v1[32];
-            tmem_ld32(t_lane + acc * C::N + k * 64, v0);
-            tmem_ld32(t_lane + acc * C::N + k * 64 + 32, v1);
-            tmem_ld_wait_regs(v0);
-            tmem_ld_wait_regs(v1);
-            if (k + C::TOKEN_WGS >= TG) {  // every TMEM read of this accumulator is complete
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&acc_empty[acc]);
-            }
-            const float* wk = w_smem + slot * TG * 64 + k * 64;
-            float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;  // four chains instead of one
-            if constexpr (kMx4) {
-              // two products per instruction (packed fp32), four weights per load
-              uint64_t a01 = 0, a23 = 0;
-#pragma unroll
-              for (int h = 0; h < 32; h += 4) {
-                const float4 wa = *reinterpret_cast<const float4*>(wk + h), wb = *reinterpret_cast<const float4*>(wk + 32 + h);
-                a01 = fma2(wa.x, wa.y, relu(v0[h]), relu(v0[h + 1]), a01);
-                a23 = fma2(wb.x, wb.y, relu(v1[h]), relu(v1[h + 1]), a23);
-                a01 = fma2(wa.z, wa.w, relu(v0[h + 2]), relu(v0[h + 3]), a01);
-                a23 = fma2(wb.z, wb.w, relu(v1[h + 2]), relu(v1[h + 3]), a23);
+            for (int k = wg / C::TILE_WGS; k < TG; k += C::TOKEN_WGS) {
+              uint32_t v0[32], v1[32];
+              tmem_ld32(t_lane + acc * C::N + k * 64, v0);
+              tmem_ld32(t_lane + acc * C::N + k * 64 + 32, v1);
+              tmem_ld_wait_regs(v0);
+              tmem_ld_wait_regs(v1);
+              if (k + C::TOKEN_WGS >= TG) {  // every TMEM read of this accumulator is complete
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[acc]);
               }
-              unpack2(a01, p0, p1);
-              unpack2(a23, p2, p3);
-            } else {
+              const float* wk = w_smem + slot * TG * 64 + k * 64;
+              float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;  // four chains instead of one
 #pragma unroll
               for (int h = 0; h < 32; h += 2) {
                 const float w0 = TG == 1 ? wreg[h] : wk[h];
@@ -974,17 +1037,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 p2 = fmaf(w2, fmaxf(__uint_as_float(v1[h]), 0.f), p2);
                 p3 = fmaf(w3, fmaxf(__uint_as_float(v1[h + 1]), 0.f), p3);
               }
-            }
-            const float score = ((p0 + p1) + (p2 + p3)) * sk;
-            const bool valid = k < grp.z && s <= grp.w + k;
-            if constexpr (kFused) {
-              // the host sizes the grid so that a CTA's items fit; the guard keeps
-              // an oversized share from writing past the buffer all the same
-              if (it - it_lo < C::CAP_ITEMS) keys[(it - it_lo) * 1024 + s - item.y * 128] = order_key(score);
-            } else {
-              if (valid) a.scores[(int64_t)(grp.y + k) * a.ld + s] = score;
-              // scores fall in random bins: a plain shared-memory add beats aggregating equal bins
-              if (do_hist && valid) atomicAdd(&sh_hist[order_key(score) >> kTopkLowBits], 1u);
+              put(((p0 + p1) + (p2 + p3)) * sk, place(s, k, grp, it, item.y));
             }
           }
         }
@@ -992,6 +1045,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         if (++acc == C::NACC) { acc = 0; aphase ^= 1; }
       }
     }
+    finish();
     __syncwarp();
   }
   tc_fence_before();
