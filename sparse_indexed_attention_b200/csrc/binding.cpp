@@ -61,7 +61,7 @@ bool fits_one(PyObject* o, PyObject* dtypes, PyObject* shape, const at::Device& 
   for (int64_t i = 0; i < t->dim(); ++i) {
     PyObject* w = PyTuple_GET_ITEM(shape, i);
     if (w == Py_None) continue;
-    const long long want = PyLong_Check(w) ? PyLong_AsLongLong(w) : -1;
+    const long long want = PyLong_AsLongLong(w);  // (any integer type)
     if (want != t->size(i)) {
       PyErr_Clear();
       return false;

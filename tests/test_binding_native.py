@@ -42,6 +42,12 @@ def test_need(bad, error, match):
 
 
 def test_need_takes_sizes_only():
+    import numpy as np
+    _binding.need(torch.zeros(4, 3), "t", (torch.float32,), (np.int64(4), np.int32(3)), CPU)
+    with pytest.raises(ValueError, match="shape"):
+        _binding.need(torch.zeros(4, 3), "t", (torch.float32,), (np.int64(3), 3), CPU)
+    with pytest.raises(ValueError, match="shape"):
+        _binding.need(torch.zeros(4), "t", (torch.float32,), ("4",), CPU)
     with pytest.raises(ValueError, match="shape"):
         _binding.need(torch.zeros(4), "t", (torch.float32,), (2 ** 70,), CPU)
     with pytest.raises(TypeError):
