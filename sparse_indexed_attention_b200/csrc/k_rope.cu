@@ -19,7 +19,7 @@
 // into shared memory and its heads share them; computed per value they would
 // cost more issue slots than the memory time allows (2 x ~40 instructions per
 // pair against 4 bytes moved per bf16 value pair at 44 B/ns per SM).
-// 8192 tokens x 64 heads x 128 dims, half of them rotated: 54 us, 76 % of the measured
+// 8192 tokens x 64 heads x 128 dims, half of them rotated: 50 us, 82 % of the measured
 // copy rate; what is left is latency (each thread has one unit in flight).
 // A thread handles 16-byte vectors where base, strides, offset and rot_dim
 // allow it, else single elements (slices at odd offsets).
@@ -67,6 +67,16 @@ __device__ __forceinline__ void rotate(E& a, E& b, float2 cs) {
   const float p = to_f(a), q = to_f(b);
   a = from_f<E>(fmaf(p, cs.x, -q * cs.y));
   b = from_f<E>(fmaf(p, cs.y, q * cs.x));
+}
+
+// Stores 16 bytes as data that this kernel does not read again (8192 tokens x 64
+// heads x 128 dims 52.3 -> 51.2 us, 1024 tokens 9.6 -> 8.6).
+template <class V>
+__device__ __forceinline__ void put(V* p, const V& v) {
+  if constexpr (sizeof(V) == 16)
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+  else
+    *p = v;
 }
 
 // One block: tb tokens x hb heads.  Work units of a (token, head) row: the
@@ -118,13 +128,13 @@ __global__ void __launch_bounds__(kThreads, 8) k_rope(const RopeArgs a) {
       if constexpr (kTwo) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) rotate(va.v[e], vb.v[e], c[e]);
-        *reinterpret_cast<V*>(o + d0 + (kHalf ? half : 1)) = vb;
+        put(reinterpret_cast<V*>(o + d0 + (kHalf ? half : 1)), vb);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) rotate(va.v[2 * e], va.v[2 * e + 1], c[e]);
       }
     }
-    *reinterpret_cast<V*>(o + d0) = va;
+    put(reinterpret_cast<V*>(o + d0), va);
   }
 }
 
@@ -148,12 +158,14 @@ cudaError_t launch_rope(const RopeCall& r, cudaStream_t st) {
                    ok(r.half_layout ? r.rot / 2 : r.rot);
   // units of a row, and a block's share: about four units per thread where the units
   // fill the GPU's threads, so that a block's angles serve more of them (8192 tokens x 64
-  // heads of 64 dims: 27.9 us, 36.6 with one unit), else one (64 x 128 heads: 2.1 us,
-  // 3.1 with four; 256 x 128: 3.7 and 3.5)
+  // heads of 64 dims: 27.9 us, 36.6 with one unit), eight where they fill them 16 times
+  // (8192 x 64 heads of 128 dims: 49.7 us, 51.2 with four; 2048: 15.7 and 15.4), else
+  // one (64 x 128 heads: 2.1 us, 3.1 with four; 256 x 128: 3.7 and 3.5)
   const int lanes = vec ? W : 1;
   const int64_t units = (r.half_layout || !vec ? r.rot / 2 / lanes : r.rot / lanes) + (a.copy ? (r.D - r.rot) / lanes : 0);
   const int64_t all = units * r.H * r.T;
-  const int64_t want = all >= (int64_t)148 * 6 * kThreads ? 4 * kThreads : kThreads;
+  const int64_t full = (int64_t)148 * 6 * kThreads;
+  const int64_t want = (all >= 16 * full ? 8 : all >= full ? 4 : 1) * kThreads;
   if (units * r.H >= want) {
     a.hb = (int)((want + units - 1) / units);
   } else {
@@ -162,7 +174,7 @@ cudaError_t launch_rope(const RopeCall& r, cudaStream_t st) {
     a.tb = (int)(t < most ? t : most);
     if (a.tb > r.T) a.tb = r.T;
   }
-  // i / units by a product: exact while i units < 2^32 (a block has at most 1024 + units units)
+  // i / units by a product: exact while i units < 2^32 (a block has at most 2048 + units units)
   if (units > 1 && units <= 16384) a.units_magic = (uint32_t)(((1ull << 32) + units - 1) / units);
   a.head_blocks = (r.H + a.hb - 1) / a.hb;
   const int64_t grid = ((int64_t)r.T + a.tb - 1) / a.tb * a.head_blocks;
