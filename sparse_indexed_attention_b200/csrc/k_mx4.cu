@@ -5,9 +5,10 @@
 // values, 16 bytes per lane on the bf16 side, 4 on the code side, so that a
 // warp's accesses are whole 128-byte lines and the group maximum is two
 // shuffles.  Four rows per thread group: one row each was bound by the start of
-// blocks (4096 x 64 rows: 18.5 us, now 15.4 us for 85 MB, 84 % of the measured copy rate;
+// blocks (4096 x 64 rows: 18.5 us, now 14.6 us for 85 MB, 89 % of the measured copy rate;
 // back: 18.1, now 10.4 us, part of it from L2).  Values pass as streaming data (read or
-// written once: a chunk's four calls 36.1 -> 32.8 us).
+// written once: a chunk's four calls 36.1 -> 32.8 us); the group's maximum is taken
+// two values at a time (31.4 us).
 #include <cuda_fp16.h>
 
 #include "mx4.cuh"

@@ -28,9 +28,9 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {  // 2^(byte - 127)
 // lane of the warp must call it.
 __device__ __forceinline__ uint32_t quantize_piece(const uint4& raw, uint32_t* scale_byte) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t m = 0;  // largest |x| as bf16 bits: NaN > infinity > finite in integer order
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  // largest |x| as bf16 bits, two values at a time: NaN > infinity > finite in integer order
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = max(m & 0xFFFFu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const bool finite = m < 0x7F80u;
