@@ -12,7 +12,8 @@
 // CTA counts its keys and adds its counts to the bins' owners through distributed
 // shared memory, and each finds the same bin by a scan.  Counts before each CTA give
 // the output offsets, so the positions come out ascending.  Latency bound: four
-// cluster barriers and the passes over the keys: 8 x 32,768 positions 14 us.
+// cluster barriers and the passes over the keys: 8 x 32,768 positions 14 us, one
+// sequence of 3001 9.9 us.
 //
 // mark.  A destination page must be no page that the call reads and no
 // destination twice, or rows would be overwritten while others still read
@@ -37,8 +38,7 @@ using topk::kD1Bins;
 using topk::kD2Bins;
 using topk::kD3Bins;
 
-constexpr int kSelThreads = 1024;
-constexpr int kCluster = 8;                    // CTAs per sequence (the portable cluster size)
+constexpr int kCluster = 8;                    // most CTAs per sequence (the portable cluster size)
 constexpr int kSlotsMax = 40960;               // keys a CTA keeps in shared memory (160 KB)
 constexpr uint32_t kForced = 0xFFFFFFFFu;      // above any key of a number
 
@@ -61,7 +61,7 @@ struct SelectSmem {
 
 // kStaged: the CTA's keys fit in shared memory; otherwise each pass reads the
 // masses again (from L2 in the main).
-template <bool kStaged>
+template <bool kStaged, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const SelectArgs a) {
   extern __shared__ uint32_t keys[];
   __shared__ SelectSmem sm;
@@ -141,16 +141,27 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const SelectArgs a
     cluster.sync();
     // from the highest digit down, `pt` digits per thread; the thread in which
     // the running count reaches `need` holds the digit
+    constexpr int kPer = kD1Bins / kSelThreads;
     const int pt = bins / kSelThreads, top = bins - 1 - tid * pt;
-    auto count = [&](int d) { return cluster.map_shared_rank(sm.total + off, d >> share)[d & mask]; };
-    const uint32_t c0 = count(top), c1 = pt == 2 ? count(top - 1) : 0u;
+    uint32_t c[kPer], sum = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int d = top - u;
+      c[u] = u < pt ? cluster.map_shared_rank(sm.total + off, d >> share)[d & mask] : 0u;
+      sum += c[u];
+    }
     uint32_t all;
-    uint32_t above = topk::block_scan(c0 + c1, sm.buf, &all);
-    if (above < need && need <= above + c0 + c1) {
-      const bool second = need > above + c0;
-      sm.bin = (uint32_t)(second ? top - 1 : top);
-      sm.above = above + (second ? c0 : 0u);
-      sm.inside = second ? c1 : c0;
+    uint32_t above = topk::block_scan(sum, sm.buf, &all);
+    if (above < need && need <= above + sum) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        if (above < need && need <= above + c[u]) {
+          sm.bin = (uint32_t)(top - u);
+          sm.above = above;
+          sm.inside = c[u];
+        }
+        above += c[u];
+      }
     }
     __syncthreads();
     prefix = (prefix << (level < 2 ? 11 : 10)) | sm.bin;
@@ -366,27 +377,42 @@ cudaError_t launch_cluster(const char* name, void (*kernel)(KArgs...), int grid,
   return e == cudaSuccess ? counted(cudaGetLastError()) : e;
 }
 
+template <int kSelThreads>
+cudaError_t launch_select(const SelectArgs& a, int B, int C, int64_t slots, cudaStream_t st) {
+  if (slots > kSlotsMax)
+    return launch_cluster("evict_select", k_evict_select<false, kSelThreads>, B * C, C, kSelThreads, 0, st, a);
+  static thread_local int attr_dev = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (attr_dev != dev) {
+    cudaError_t e = cudaFuncSetAttribute(k_evict_select<true, kSelThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSlotsMax * 4);
+    if (e != cudaSuccess) return e;
+    attr_dev = dev;
+  }
+  return launch_cluster("evict_select", k_evict_select<true, kSelThreads>, B * C, C, kSelThreads, (size_t)slots * 4, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_evict_select(const int32_t* ctx_len, int B, int max_ctx, const int64_t* mass, int64_t ld, int budget,
                                 int recent, int sink, int32_t* keep, int32_t* keep_len, uint32_t* err,
                                 cudaStream_t st) {
   const SelectArgs a{ctx_len, mass, ld, max_ctx, budget, recent, sink, keep, keep_len, err};
-  // a short row is one CTA's work: cluster barriers would only add latency (1000
-  // positions: 9.0 us alone, 10.1 as a cluster; 3001: 11.3 and 10.6; 32,768: 57 and 17)
-  const int C = max_ctx <= 2 * kSelThreads ? 1 : kCluster;
-  const int64_t slots = (((int64_t)max_ctx + C - 1) / C + 3) & ~3;
-  if (slots > kSlotsMax) return launch_cluster("evict_select", k_evict_select<false>, B * C, C, kSelThreads, 0, st, a);
-  static thread_local int attr_dev = -1;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (attr_dev != dev) {
-    cudaError_t e =
-        cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotsMax * 4);
-    if (e != cudaSuccess) return e;
-    attr_dev = dev;
-  }
-  return launch_cluster("evict_select", k_evict_select<true>, B * C, C, kSelThreads, (size_t)slots * 4, st, a);
+  // A cluster's size: about 1024 positions per CTA (one sequence of 1000: 8.2 us alone,
+  // 8.7 with two CTAs; 3001: 12.6 alone, 9.9 with four; 32,768: 56 and 15 with
+  // eight), as far as all CTAs find an SM of their own (64 x 3001: 12.4 us with two, 29.6
+  // with eight; 32 x 32,768: 24.4 with four, 44 with eight), and no smaller than
+  // keeps the keys in shared memory.  512 threads while each takes at most four keys or
+  // shares its SM (cheaper barriers; 3001 by four: 9.9 for 10.4 us), else 1024
+  // (32,768 by eight: 15.0 for 16.6).
+  auto slots = [&](int C) { return (((int64_t)max_ctx + C - 1) / C + 3) & ~(int64_t)3; };
+  int C = 1;
+  while (C < kCluster && slots(C) > 1024) C *= 2;
+  while (C > 1 && (int64_t)B * C > 148) C /= 2;
+  while (C < kCluster && slots(C) > kSlotsMax) C *= 2;
+  const bool few = slots(C) <= 4 * 512 || (int64_t)B * C > 148;
+  return few ? launch_select<512>(a, B, C, slots(C), st) : launch_select<1024>(a, B, C, slots(C), st);
 }
 
 size_t evict_bitmap_bytes(int pages) { return (size_t)3 * (((size_t)pages + 31) / 32) * 4; }

@@ -276,6 +276,20 @@ def test_select(lib, n, budget, recent, sink, kind):
     assert np.array_equal(keep.cpu().numpy(), ref)
 
 
+@pytest.mark.parametrize("kind", ["few", "heavy"])
+@pytest.mark.parametrize("B,n", [(3, 1024), (2, 1025), (5, 2049), (40, 3001), (75, 2500), (149, 1500), (300, 700),
+                                 (19, 9000), (80, 45000)])
+def test_select_batches(lib, B, n, kind):
+    """Every size of cluster and block that batches of these sizes take."""
+    budget, recent, sink = n // 3, 17, 3
+    ctx = [n - 5 * b % (n - budget // 2) for b in range(B)]
+    mass = _masses(B, n + 1, kind)
+    keep, lens = lib.dsa_evict_select(torch.tensor(ctx, dtype=torch.int32).cuda(), mass.cuda(), budget, recent, sink)
+    ref, ref_len = S.evict_select(ctx, mass.numpy(), budget, recent, sink)
+    assert np.array_equal(lens.cpu().numpy(), ref_len)
+    assert np.array_equal(keep.cpu().numpy(), ref)
+
+
 @pytest.mark.parametrize("extra", [-3, 0, 1003])
 def test_select_past_shared_memory(lib, extra):
     """A sequence whose keys do not fit the cluster's shared memory is read again instead."""
