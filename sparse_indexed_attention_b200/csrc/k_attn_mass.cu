@@ -16,7 +16,7 @@
 //     row's five is half of one) at a time, into a ring of 128-byte-swizzled operand
 //     slots, each with its own barriers: the query (H x 1152 bytes) fills most of
 //     shared memory, and the ring keeps loads in flight across blocks;
-//   * two threads, taking tiles in turn, issue the MMAs, eight per tile, each
+//   * two warps, taking tiles in turn, issue the MMAs, eight per tile, each
 //     tile into an accumulator of its own (a ring of four): the waits, fence, issue and
 //     commits are one serial chain per tile, and two of them overlap;
 //   * eight warps, two per lane quarter with half of the heads each, add the
@@ -59,7 +59,7 @@ constexpr int kAtoms = kDQK / 64;            // 9 slices of 64 dims
 constexpr int kAtomBytes = kRows * 128;
 constexpr int kTiles = 5;                    // of a row: two atoms each, the last one
 constexpr int kSumWarps = 8;                 // warps 0-7
-constexpr int kIssuers = 2;                  // warps 8-9, one thread each; warp 8 owns TMEM
+constexpr int kIssuers = 2;                  // warps 8-9, an elected lane of each; warp 8 owns TMEM
 constexpr int kLoaderBarrier = 1, kSumBarrier = 2;
 constexpr int kMmaWarp = kSumWarps;
 constexpr int kLoadWarp = kMmaWarp + kIssuers;
