@@ -27,6 +27,7 @@
 // measured copy rate in between.
 #include <cooperative_groups.h>
 
+#include "row_of.cuh"
 #include "topk_select.cuh"
 
 namespace dsa {
@@ -221,7 +222,7 @@ struct MoveArgs {
   const uint8_t* src[DSA_MAX_POOLS];
   uint8_t* dst[DSA_MAX_POOLS];
   int row_bytes[DSA_MAX_POOLS], vec[DSA_MAX_POOLS];
-  uint32_t magic[DSA_MAX_POOLS];
+  RowDivisor by[DSA_MAX_POOLS];  // a row's vectors (at most 16,384, and 32 rows a block)
   const int64_t* mass;
   int64_t* new_mass;
   int64_t ld, new_ld;
@@ -268,19 +269,19 @@ __global__ void __launch_bounds__(1024) k_evict_mark(const MoveArgs a) {
   }
 }
 
-// Rows of V vectors, nv per row: element i of the block's page is vector i % nv of its
-// row i / nv (by a product with `magic` = ceil(2^32 / nv): exact for i < 64 nv, nv <= 2^14).
+// Rows of V vectors: element i of the block is vector i % nv of its row i / nv.
 template <class V>
 struct RowsOf {
   const uint8_t* src;
   uint8_t* dst;
-  int row_bytes, nv, total;
-  uint32_t magic;
+  int row_bytes, total;
+  RowDivisor by;
   __device__ __forceinline__ bool load(int i, const int* rows, V* v) const {
     if (i >= total) return false;
-    const int r = nv == 1 ? i : (int)__umulhi((uint32_t)i, magic), c = i - r * nv, row = rows[r];
+    const RowColumn at = row_of((uint32_t)i, by);
+    const int row = rows[at.row];
     if (row < 0) return false;
-    *v = __ldcs(reinterpret_cast<const V*>(src + (int64_t)row * row_bytes) + c);  // read once, as it is written
+    *v = __ldcs(reinterpret_cast<const V*>(src + (int64_t)row * row_bytes) + (int)at.column);  // read once, as it is written
     return true;
   }
   __device__ __forceinline__ void store(int i, const V& v) const { __stcs(reinterpret_cast<V*>(dst) + i, v); }
@@ -304,7 +305,8 @@ __device__ __forceinline__ void move_rows(const RowsOf<V>& m, const int* rows) {
 template <class V>
 __device__ __forceinline__ void move_pool(const MoveArgs& a, int k, int64_t first_row, const int* rows, int n) {
   const int nv = a.row_bytes[k] / (int)sizeof(V);
-  move_rows(RowsOf<V>{a.src[k], a.dst[k] + first_row * a.row_bytes[k], a.row_bytes[k], nv, n * nv, a.magic[k]}, rows);
+  move_rows(RowsOf<V>{a.src[k], a.dst[k] + first_row * a.row_bytes[k], a.row_bytes[k], n * nv,
+                      RowDivisor{(uint32_t)nv, a.by[k].magic, a.by[k].add}}, rows);
 }
 
 // One block: kMoveRows rows of sequence b's new cache, from row i0.  They are
@@ -433,8 +435,7 @@ cudaError_t launch_evict_compact(const SeqsDev& s, const EvictMove& m, void* bit
     a.dst[k] = static_cast<uint8_t*>(p.dst);
     a.row_bytes[k] = p.row_bytes;
     a.vec[k] = p.row_bytes % 16 == 0 ? 16 : (p.row_bytes % 8 == 0 ? 8 : 4);
-    const uint32_t nv = (uint32_t)(p.row_bytes / a.vec[k]);
-    a.magic[k] = nv == 1 ? 0u : (uint32_t)(((1ull << 32) + nv - 1) / nv);
+    a.by[k] = row_divisor((uint32_t)(p.row_bytes / a.vec[k]));
     a.in_place = a.in_place || p.src == p.dst;
   }
   a.mass = m.mass;

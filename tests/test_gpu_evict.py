@@ -414,3 +414,25 @@ def test_compact_refuses_pages_in_use(lib):
     got, st = run(new_table, lens=bad_len)
     assert st == lib.DSA_ERR_BAD_INDEX and torch.equal(got[r(new_table[0, 0])], pool0[r(new_table[0, 0])])
     assert run(new_table)[1] == lib.DSA_OK         # the same workspace, clean again
+
+
+@pytest.mark.parametrize("inside", [True, False])
+@pytest.mark.parametrize("row_bytes", [46508, 65528, 65532, 65536])
+def test_compact_wide_rows(lib, row_bytes, inside):
+    """Rows up to the largest, whole blocks of them and part of one."""
+    ctx, budget = [70, 33, 5], 40
+    table, new_table, total = _cache(ctx, 1)
+    seqs = _seqs(lib, ctx, table, total)
+    keep, lens = lib.dsa_evict_select(seqs.ctx_len, _masses(3, 70, "heavy").cuda(), budget)
+    assert lens.tolist() == [40, 33, 5]
+    src = torch.randint(0, 256, (total * 64, row_bytes), generator=torch.Generator("cuda").manual_seed(row_bytes),
+                        dtype=torch.uint8, device="cuda")
+    dst = src if inside else torch.full_like(src, 7)
+    want = dst.clone()
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    for b, n in enumerate(lens.tolist()):
+        to = torch.from_numpy(_rows(new_table[b], np.arange(n))).cuda()
+        want[to] = src[torch.from_numpy(_rows(table[b], keep[b, :n].cpu().numpy().astype(np.int64))).cuda()]
+    lib.dsa_evict_compact(seqs, keep, lens, torch.from_numpy(new_table).cuda(), [src if inside else (src, dst)], ws=ws)
+    assert lib.dsa_check_error(ws) == lib.DSA_OK
+    assert torch.equal(dst, want)
