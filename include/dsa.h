@@ -267,7 +267,9 @@ dsa_status_t dsa_dequantize_mx4(const uint8_t *codes, const uint8_t *scales,
  * MXFP8 cache: kI[s,32g..32g+31] = E4M3(codes) * 2^(kI_scale[s,g] - 127) and qI
  * is first quantized as in dsa_quantize_index_query_mx; the group scales are
  * applied by the tensor core's block-scaled MMA.  MXFP4 cache: likewise with E2M1
- * codes and dsa_quantize_index_query_mx4.
+ * codes and dsa_quantize_index_query_mx4; a scale byte of 255 (NaN) in a key or in
+ * a query row makes the scores it enters NaN.  (In the other formats the ReLU of a
+ * NaN product counts as 0.)
  * Entries s > pos(t) of a row are left untouched.  ld >= max_ctx.
  * The reduction over heads happens in the kernel; no [T,H_I,N] tensor exists.
  *   qI bf16 [T,64,128]; w fp32 [T,64]; kI pool; kI_scale fp32 [R], uint8
@@ -283,7 +285,8 @@ dsa_status_t dsa_index_scores(const dsa_seqs_t *seqs, const void *qI,
  * scores[t*ld + 0 .. row_len[t]-1].  idx[t*K + 0 ..] receives the positions of
  * the min(K, row_len[t]) largest scores -- equal scores prefer the lower
  * position, -0.0 equals +0.0 -- in ASCENDING order, padded with -1.  The
- * result is exactly determined (bit-exact).  NaN scores are not supported.
+ * result is exactly determined (bit-exact).  NaN scores are not supported: they
+ * rank by their bits, those of the MXFP4 indexer above every number.
  * A row_len outside 0..ld sets DSA_ERR_BAD_INDEX (the row is clamped). */
 dsa_status_t dsa_topk(const float *scores, int64_t ld, int T,
                       const int32_t *row_len, int K, int32_t *idx, void *ws,

@@ -543,7 +543,12 @@ __device__ void fused_topk_tail(const IdxArgs& a, uint32_t* keys, int it_lo, int
   }
 }
 
-__device__ __forceinline__ float relu(uint32_t bits) { return fmaxf(__uint_as_float(bits), 0.f); }
+// max(x, 0); a NaN stays one (MXFP4 has scales that stand for it).
+__device__ __forceinline__ float relu(uint32_t bits) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(bits)));
+  return y;
+}
 
 // {a0, a1} * {b0, b1} + c as two fp32 lanes of one instruction.
 __device__ __forceinline__ uint64_t fma2(float a0, float a1, float b0, float b1, uint64_t c) {

@@ -199,3 +199,39 @@ def test_whole_path(lib, name, select):
     ref = S.index_scores_mx4(P.oracle_seqs(wl), bits16(wl.qI), wl.w.numpy(), kI, sc, tokens=tokens)
     for t, r in zip(tokens, ref):
         assert not P.selection_violations(idx[t].cpu().numpy(), r, K)
+
+
+@pytest.mark.parametrize("name", ["decode_small", "chunked_small"])
+def test_a_nan_block_makes_its_scores_nan(lib, name):
+    """A key or a query with an infinity or NaN: scale byte 255 in its block, NaN in the
+    scores that block enters, and nowhere else."""
+    import dataclasses
+    wl, kI, sc = _workload(name)
+    seqs, d = P.oracle_seqs(wl), to_device(wl)
+    k = torch.randn(wl.T, 128, generator=torch.Generator().manual_seed(3)).bfloat16()
+    k[0, 40], k[1, 100] = float("nan"), -float("inf")
+    q = wl.qI.clone()
+    q[2, 5, 17] = float("inf")
+    wl = dataclasses.replace(wl, qI=q)
+    kI_d, sc_d = torch.from_numpy(kI).cuda(), torch.from_numpy(sc).cuda()
+    lib.dsa_append_index_keys_mx4(d.seqs, k.cuda(), kI_d, sc_d)
+    kI, sc = kI_d.cpu().numpy(), sc_d.cpu().numpy()
+    got = lib.dsa_index_scores(d.seqs, q.cuda(), d.w, kI_d, sc_d).cpu().numpy()
+    tokens = np.arange(wl.T) if wl.T <= 64 else np.unique([0, 1, 2, 3, *P.sample_tokens(wl, 16)])
+    seen = 0
+    for t, r in zip(tokens, S.index_scores_mx4(seqs, bits16(q), wl.w.numpy(), kI, sc, tokens=tokens)):
+        nan = np.isnan(r)
+        assert np.array_equal(np.isnan(got[t, :len(r)]), nan), t
+        tol = _score_tolerance(wl, kI, sc, t)
+        assert (np.abs(got[t, :len(r)] - r)[~nan] <= tol[~nan]).all()
+        seen += nan.any()
+        assert nan.all() == (t == 2)
+    assert seen >= 3
+    # the selection takes such a position before every number
+    K = min(32, wl.spec.topk)
+    for select in (False, True) if wl.T == wl.spec.batch else (False,):
+        idx = torch.empty((wl.T, K), dtype=torch.int32, device="cuda")
+        lib.dsa_index_topk_attn(d.seqs, q.cuda(), d.w, kI_d, sc_d, d.q, d.kv, K, wl.scale, idx_out=idx,
+                                select_in_indexer=select)
+        for t in (0, 1):
+            assert int(wl.token_pos()[t]) in idx[t].tolist()
