@@ -289,6 +289,10 @@ _ws_captured: dict = {}
 def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     """A zeroed device workspace of at least nbytes, cached per (device, key).
 
+    The calls' keys: "index_scores", "topk", "sparse_mla", "index_topk_attn",
+    "append_index_keys", "attn_mass", "evict_select" and "evict_compact".
+    workspace(0, device, key) is the buffer whose error flag dsa_check_error reads.
+
     Every call that is not given `ws` uses this cached buffer, whatever its
     stream.  Calls that may run at the same time on different streams must
     each pass a workspace of their own: the library requires that concurrent
@@ -585,8 +589,7 @@ def dsa_evict_compact(seqs: Seqs, keep, keep_len, new_page_table, pools, mass=No
         _need(new_mass, "new_mass", _I64T, (B, None), dev)
         ld, new_ld = mass.shape[1], new_mass.shape[1]
     need = 256 + (3 * ((new_pages + 31) // 32) * 4 + 255) // 256 * 256
-    # one cached buffer per size: a captured call's buffer is never replaced by a larger one
-    ws = _space(ws, need, dev, ("evict_compact", need))
+    ws = _space(ws, need, dev, "evict_compact")
     _check(_binding.dsa_evict_compact(dev, seqs, keep, keep_len, keep.shape[1], new_page_table, new_page_table.shape[1],
                                       new_pages, c_pools, len(pools), mass, ld, new_mass, new_ld, ws, ws.numel()),
            "dsa_evict_compact")

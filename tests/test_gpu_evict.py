@@ -436,3 +436,19 @@ def test_compact_wide_rows(lib, row_bytes, inside):
     lib.dsa_evict_compact(seqs, keep, lens, torch.from_numpy(new_table).cuda(), [src if inside else (src, dst)], ws=ws)
     assert lib.dsa_check_error(ws) == lib.DSA_OK
     assert torch.equal(dst, want)
+
+
+def test_default_workspace_tells_of_a_refused_page(lib):
+    """The error flag of calls without a workspace is where the other operators have it,
+    whatever the pools' sizes."""
+    flag = lambda: lib.dsa_check_error(lib.workspace(0, "cuda", "evict_compact"))  # noqa: E731
+    for ctx in ([300, 200], [70], [30000, 5]):
+        table, new_table, total = _cache(ctx, 1)
+        seqs = _seqs(lib, ctx, table, total)
+        keep, lens = lib.dsa_evict_select(seqs.ctx_len, _masses(len(ctx), max(ctx), "heavy").cuda(), 50)
+        pool = torch.randn((total * 64, 8)).cuda()
+        lib.dsa_evict_compact(seqs, keep, lens, torch.from_numpy(new_table).cuda(), [pool])
+        assert flag() == lib.DSA_OK
+        new_table[0, 0] = table[0, 0]
+        lib.dsa_evict_compact(seqs, keep, lens, torch.from_numpy(new_table).cuda(), [pool])
+        assert flag() == lib.DSA_ERR_BAD_INDEX and flag() == lib.DSA_OK

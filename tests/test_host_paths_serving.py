@@ -49,3 +49,38 @@ def test_entry_points_return_without_a_gpu(host_binding, T, heads, kv_fp8):
     for call in calls:
         with pytest.raises(dsa.DsaError, match="DSA_ERR_CUDA"):
             call()
+
+
+def test_default_workspaces_have_the_documented_keys(monkeypatch):
+    """workspace(0, device, key) finds the buffer of a call that was given none."""
+    used = []
+
+    def workspace(n, dev, key=None):
+        used.append(key)
+        return _aligned(torch.zeros(max(n, 256), dtype=torch.uint8))
+    monkeypatch.setattr(dsa, "_cuda_device", lambda t, name: t.device)
+    documented = dsa.workspace.__doc__
+    monkeypatch.setattr(dsa, "workspace", workspace)
+    z = lambda *s, dt=torch.float32: _aligned(torch.zeros(s, dtype=dt))  # noqa: E731
+    u8, bf, i32, i64 = torch.uint8, torch.bfloat16, torch.int32, torch.int64
+    seqs = dsa.Seqs(_aligned(torch.tensor([0, 1], dtype=i32)), _aligned(torch.tensor([100], dtype=i32)),
+                    z(1, 2, dt=i32), 8, 100, 1)
+    R = 8 * 64
+    kI, kI_scale, kv, mass, keep = z(R, 64, dt=u8), z(R, 4, dt=u8), z(R, 576, dt=bf), z(1, 128, dt=i64), z(1, 64, dt=i32)
+    q, idx, lse = z(1, 16, 576, dt=bf), z(1, 64, dt=i32), z(1, 16)
+    calls = {
+        "append_index_keys": lambda: dsa.dsa_append_index_keys_mx4(seqs, z(1, 128, dt=bf), kI, kI_scale),
+        "index_scores": lambda: dsa.dsa_index_scores(seqs, z(1, 64, 128, dt=bf), z(1, 64), kI, kI_scale, scores=z(1, 128)),
+        "topk": lambda: dsa.dsa_topk(z(1, 128), z(1, dt=i32), 64, idx=idx),
+        "sparse_mla": lambda: dsa.dsa_sparse_mla_fwd(seqs, q, kv, idx, 0.04, out=z(1, 16, 512, dt=bf), lse=lse),
+        "index_topk_attn": lambda: dsa.dsa_index_topk_attn(seqs, z(1, 64, 128, dt=bf), z(1, 64), kI, kI_scale, q, kv, 64,
+                                                           0.04, out=z(1, 16, 512, dt=bf), lse=lse),
+        "attn_mass": lambda: dsa.dsa_attn_mass(seqs, q, kv, idx, lse, 0.04, mass),
+        "evict_select": lambda: dsa.dsa_evict_select(seqs.ctx_len, mass, 64, keep=keep, keep_len=z(1, dt=i32)),
+        "evict_compact": lambda: dsa.dsa_evict_compact(seqs, keep, z(1, dt=i32), z(1, 1, dt=i32), [kI, (kv, z(R, 576, dt=bf))]),
+    }
+    for key, call in calls.items():
+        used.clear()
+        with pytest.raises(dsa.DsaError, match="DSA_ERR_CUDA"):
+            call()
+        assert used == [key] and f'"{key}"' in documented
