@@ -8,13 +8,13 @@ raises.
 
 Functions carry the C names (``dsa_index_scores`` ...).  Outputs not passed in
 are allocated with torch on the inputs' device; workspaces are allocated
-zeroed and cached per (device, op), unless one is passed in (concurrent
-calls on different streams pass their own).
+zeroed and cached per device, op, host thread and stream, unless one is passed in.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -282,38 +282,51 @@ def dsa_workspace_size(op: int, seqs: Seqs | None = None, K: int = 1, H: int = 1
     return int(_lib.dsa_workspace_size(op, ctypes.byref(c), K, H))
 
 
-_ws_cache: dict = {}
+_ws_own = threading.local()     # .cache: (device, stream, key) -> buffer
+_ws_newest: dict = {}           # (device, key) -> the buffer made last, by whatever thread and for whatever stream
 _ws_captured: dict = {}
 
 
 def workspace(nbytes: int, device, key=None) -> torch.Tensor:
-    """A zeroed device workspace of at least nbytes, cached per (device, key).
+    """A zeroed device workspace of at least nbytes, cached per (device, key) for
+    the calling thread and the device's current stream.
 
     The calls' keys: "index_scores", "topk", "sparse_mla", "index_topk_attn",
     "append_index_keys", "attn_mass", "evict_select" and "evict_compact".
-    workspace(0, device, key) is the buffer whose error flag dsa_check_error reads.
+    workspace(0, device, key) is the buffer whose error flag dsa_check_error
+    reads: that of this thread and stream, or the newest if they have none.
 
-    Every call that is not given `ws` uses this cached buffer, whatever its
-    stream.  Calls that may run at the same time on different streams must
-    each pass a workspace of their own: the library requires that concurrent
-    calls do not share one (its first word is the sticky error flag).
+    Every call that is not given `ws` uses this buffer, so that calls of two
+    threads or streams do not share one (the library requires that of concurrent
+    calls: scratch and sticky error flag are in it).
 
-    During stream capture a buffer that is not cached yet belongs to the graph
-    alone (its zeroing is part of the graph and has not run), so it is not
-    cached; a captured call whose error flag is to be read passes its own.  A
-    cached buffer that a capture uses stays alive when a larger one replaces it:
-    the graph still writes to it."""
+    During stream capture the newest buffer serves where the capturing stream has none,
+    and one that has to be made belongs to the graph alone (its zeroing is part
+    of the graph and has not run), so it is not cached.  A graph that is replayed
+    beside other calls or graphs, or whose error flag is to be read, is captured
+    with a workspace of its own.  A cached buffer that a capture uses stays alive
+    when a larger one replaces it: the graph still writes to it."""
     if not isinstance(device, torch.device):
         device = torch.device(device)
-    if device.index is None and device.type == "cuda":
-        device = torch.device("cuda", torch.cuda.current_device())
-    k = (device, key)
-    ws = _ws_cache.get(k)
-    capturing = device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing()
+    capturing = False
+    if device.type == "cuda":
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        k = (device.index, torch._C._cuda_getCurrentRawStream(device.index), key)
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+    else:
+        k = (device, None, key)
+    try:
+        cache = _ws_own.cache
+    except AttributeError:
+        cache = _ws_own.cache = {}
+    ws = cache.get(k)
+    if ws is None and (capturing or nbytes == 0):
+        ws = _ws_newest.get((device, key))
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         if not capturing:
-            _ws_cache[k] = ws
+            cache[k] = _ws_newest[device, key] = ws
     elif capturing:
         _ws_captured[ws.data_ptr()] = ws
     return ws
