@@ -324,8 +324,10 @@ def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     if ws is None and (capturing or nbytes == 0):
         ws = _ws_newest.get((device, key))
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        small, ws = ws, torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         if not capturing:
+            if small is not None:
+                ws[:4].copy_(small[:4])     # an error that was not read yet
             cache[k] = _ws_newest[device, key] = ws
     elif capturing:
         _ws_captured[ws.data_ptr()] = ws

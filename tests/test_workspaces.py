@@ -122,3 +122,23 @@ def test_two_at_once_without_workspaces(threads):
     for a, b in zip(want, got):
         for i, x in enumerate(b):
             assert torch.equal(x, a[i % 4]), i
+
+
+def test_a_larger_buffer_keeps_the_error_flag():
+    small = dsa.workspace(512, "cpu", "keeps_the_flag")
+    small[:8] = torch.tensor([2, 0, 0, 0, 9, 9, 9, 9], dtype=torch.uint8)
+    large = dsa.workspace(4096, "cpu", "keeps_the_flag")
+    assert large.numel() == 4096 and large[0] == 2 and not large[1:].any()
+
+
+@pytest.mark.gpu
+def test_an_error_outlives_a_larger_call():
+    flag = lambda: dsa.dsa_check_error(dsa.workspace(0, "cuda", "topk"))  # noqa: E731
+    with torch.cuda.stream(torch.cuda.Stream()):           # a stream without workspaces
+        scores = torch.randn(2, 64, device="cuda")
+        dsa.dsa_topk(scores, torch.tensor([65, 64], dtype=torch.int32, device="cuda"), 8)     # a row too long
+        before = dsa.workspace(0, "cuda", "topk").numel()
+        scores = torch.randn(2, 100_000, device="cuda")
+        dsa.dsa_topk(scores, torch.full((2,), 100_000, dtype=torch.int32, device="cuda"), 8)
+        assert dsa.workspace(0, "cuda", "topk").numel() > before
+        assert flag() == dsa.DSA_ERR_BAD_INDEX and flag() == dsa.DSA_OK
