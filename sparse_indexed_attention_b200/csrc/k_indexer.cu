@@ -930,15 +930,20 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       for (int i = lane; i < kTopkHistBins; i += 32) sh_hist[i] = 0u;
       __syncwarp();
     }
-    // where key s's score for the group's token k goes, or -1
-    auto place = [&](int s, int k, const int4& grp, int it, int item_tile) -> int64_t {
+    // Whether key s's score for the group's token k is wanted, where it goes, and
+    // taking it there.  (An address of -1 for the unwanted ones costs prompts 3 to 4 % where
+    // no address is kept: E4M3, 8192 tokens, 651 for 630 us.)
+    auto wanted = [&](int s, int k, const int4& grp, int it) {
       // the host sizes the grid so that a CTA's items fit; the guard keeps
       // an oversized share from writing past the buffer all the same
-      if constexpr (kFused) return it - it_lo < C::CAP_ITEMS ? (it - it_lo) * 1024 + s - item_tile * 128 : -1;
-      return k < grp.z && s <= grp.w + k ? (int64_t)(grp.y + k) * a.ld + s : -1;
+      if constexpr (kFused) return it - it_lo < C::CAP_ITEMS;
+      return k < grp.z && s <= grp.w + k;
+    };
+    auto place = [&](int s, int k, const int4& grp, int it, int item_tile) -> int64_t {
+      if constexpr (kFused) return (it - it_lo) * 1024 + s - item_tile * 128;
+      return (int64_t)(grp.y + k) * a.ld + s;
     };
     auto put = [&](float score, int64_t at) {
-      if (at < 0) return;
       if constexpr (kFused) {
         keys[at] = order_key(score);
       } else {
@@ -956,7 +961,10 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     bool pending = false;
     auto finish = [&] {
       if constexpr (C::PIPED) {
-        if (pending) put(pend_sum + weigh32(vb, wreg + 32), pend_at);
+        if (pending) {
+          const float score = pend_sum + weigh32(vb, wreg + 32);
+          if (pend_at >= 0) put(score, pend_at);
+        }
         pending = false;
       }
     };
@@ -1010,7 +1018,7 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             tmem_ld_wait_regs(va);
             tmem_ld32(t_lane + acc * C::N + k * 64 + 32, vb);
             pend_sum = weigh32(va, wreg);
-            pend_at = place(s, k, grp, it, item.y);
+            pend_at = wanted(s, k, grp, it) ? place(s, k, grp, it, item.y) : -1;
             pending = true;
             tmem_ld_wait_regs(vb);
             tc_fence_before();
@@ -1042,7 +1050,8 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 p2 = fmaf(w2, fmaxf(__uint_as_float(v1[h]), 0.f), p2);
                 p3 = fmaf(w3, fmaxf(__uint_as_float(v1[h + 1]), 0.f), p3);
               }
-              put(((p0 + p1) + (p2 + p3)) * sk, place(s, k, grp, it, item.y));
+              const float score = ((p0 + p1) + (p2 + p3)) * sk;
+              if (wanted(s, k, grp, it)) put(score, place(s, k, grp, it, item.y));
             }
           }
         }
