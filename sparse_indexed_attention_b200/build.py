@@ -21,6 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(PKG, "_binding.built_for")     # the torch and Python that _binding.so was compiled against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -43,11 +44,35 @@ def _inputs() -> list[str]:
         BINDING_SRC, os.path.abspath(__file__)]
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+def target() -> str:
+    """The torch and Python whose C++ layouts _binding.so takes from their headers."""
+    import sysconfig
+
+    import torch
+
+    return (f"torch {torch.__version__} {torch.version.git_version} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"{sysconfig.get_config_var('SOABI')}\n")
+
+
+def _newer_input(than: str) -> bool:
+    t = os.path.getmtime(than)
     return any(os.path.getmtime(p) > t for p in _inputs())
+
+
+def library_is_stale() -> bool:
+    return not os.path.exists(LIB) or _newer_input(LIB)
+
+
+def binding_is_stale() -> bool:
+    """Also where it was built for another torch or Python: it would read their objects wrongly."""
+    if not os.path.exists(BINDING) or not os.path.exists(BUILT_FOR) or _newer_input(BINDING):
+        return True
+    with open(BUILT_FOR) as f:
+        return f.read() != target()
+
+
+def is_stale() -> bool:
+    return library_is_stale() or binding_is_stale()
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -56,9 +81,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with open(os.path.join(BUILD, ".lock"), "w") as lock:
         fcntl.flock(lock, fcntl.LOCK_EX)          # concurrent importers build once
-        if not force and not is_stale():
-            return LIB
-        return _build(verbose)
+        if force or library_is_stale():
+            _build_library(verbose)
+        if force or binding_is_stale():
+            _build_binding()
+        return LIB
 
 
 def _binding_command(out: str) -> list[str]:
@@ -78,7 +105,7 @@ def _binding_command(out: str) -> list[str]:
             "-L", PKG, "-l:libdsa.so", "-Wl,-rpath,$ORIGIN"]
 
 
-def _build(verbose: bool) -> str:
+def _build_library(verbose: bool) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if verbose else []
 
@@ -99,12 +126,19 @@ def _build(verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def _build_binding() -> None:
     tmp = BINDING + ".tmp"
     r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    if os.path.exists(BUILT_FOR):
+        os.remove(BUILT_FOR)
     os.replace(tmp, BINDING)
-    return LIB
+    with open(BUILT_FOR + ".tmp", "w") as f:
+        f.write(target())
+    os.replace(BUILT_FOR + ".tmp", BUILT_FOR)
 
 
 if __name__ == "__main__":
