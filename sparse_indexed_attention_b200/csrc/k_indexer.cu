@@ -829,7 +829,8 @@ k_index_scores_tc(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const int p = C::NISS == 2 ? __shfl_sync(0xffffffffu, warp, 0) - 1 : 0;  // this issuer's tile of each stage
       int stage = 0, sphase = 0, acc = p, aphase = 0, prev_g = -1, gcount = 0, slot = 0;
       int4 nb = it_lo < it_hi ? recs[2 * rec_of(it_lo) + 1] : make_int4(0, 0, 0, 0);
-      for (int it = it_lo; it < it_hi && !*abort_flag; ++it) {
+      // (another warp may raise the flag between two lanes' looks at it: they leave together)
+      for (int it = it_lo; it < it_hi && __all_sync(0xffffffffu, !*abort_flag); ++it) {
         const int4 item = make_int4(nb.z, nb.x, nb.y, 0);  // {g, tile_begin, tile_end}
         if (it + 1 < it_hi) nb = recs[2 * rec_of(it + 1) + 1];
         if (item.x != prev_g) {

@@ -235,3 +235,39 @@ def test_a_nan_block_makes_its_scores_nan(lib, name):
                                 select_in_indexer=select)
         for t in (0, 1):
             assert int(wl.token_pos()[t]) in idx[t].tolist()
+
+
+@pytest.mark.parametrize("select", [False, True])
+@pytest.mark.parametrize("name", ["decode_small", "chunked_small", "many_items"])
+def test_short_wait_limit_winds_down(lib, name, select):
+    """A wait limit of 1 ns: producers, issuers and epilogue give up by themselves and say
+    so (or were fast enough); the next calls are clean and give the same bits as before."""
+    wl, kI, sc = _workload(name)
+    if select and wl.T != wl.spec.batch:
+        pytest.skip("the selection inside the indexer serves decode batches")
+    d, K = to_device(wl), wl.spec.topk
+    kI_d, sc_d = torch.from_numpy(kI).cuda(), torch.from_numpy(sc).cuda()
+    op = lib.DSA_OP_INDEX_TOPK_ATTN_FUSED if select else lib.DSA_OP_INDEX_TOPK_ATTN
+    spaces = [torch.zeros(lib.dsa_workspace_size(o, d.seqs, K, wl.spec.heads), dtype=torch.uint8, device="cuda")
+              for o in (lib.DSA_OP_INDEX_SCORES, op)]
+
+    def scores():
+        return lib.dsa_index_scores(d.seqs, d.qI, d.w, kI_d, sc_d, ws=spaces[0])
+
+    def path():
+        idx = torch.empty((wl.T, K), dtype=torch.int32, device="cuda")
+        out, lse = lib.dsa_index_topk_attn(d.seqs, d.qI, d.w, kI_d, sc_d, d.q, d.kv, K, wl.scale, idx_out=idx, ws=spaces[1],
+                                           select_in_indexer=select)
+        return idx, out, lse
+    want = scores(), *path()
+    assert [lib.dsa_check_error(w) for w in spaces] == [lib.DSA_OK] * 2
+    for _ in range(5):
+        lib.dsa_set_wait_limit_ns(1)
+        try:
+            scores()
+            path()
+        finally:
+            lib.dsa_set_wait_limit_ns(0)
+        assert all(lib.dsa_check_error(w) in (lib.DSA_OK, lib.DSA_ERR_TIMEOUT) for w in spaces)
+        assert all(torch.equal(a, b) for a, b in zip(want, (scores(), *path())))
+        assert [lib.dsa_check_error(w) for w in spaces] == [lib.DSA_OK] * 2
