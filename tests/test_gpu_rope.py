@@ -125,3 +125,29 @@ def test_large_and_captured(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and lib.dsa_launches_in_last_call() == 1
+
+
+@pytest.mark.parametrize("T,H,D,rot,offset", [(4743, 67, 128, 64, 32), (1801, 37, 97, 66, 5)])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_the_largest_calls(lib, T, H, D, rot, offset, interleaved):
+    """Ragged calls of more than 16 x 148 x 6 x 256 units, whose blocks take eight units per
+    thread: the bits of calls on a few tokens each, and the oracle's values on some rows."""
+    c = (T, H, D, rot, offset, interleaved, "linear", 4.0)
+    units = (rot // 16 if D % 8 == 0 and not interleaved else rot // 8 if D % 8 == 0 else rot // 2) \
+        + (D - rot) // (8 if D % 8 == 0 else 1)
+    assert units * T * H >= 16 * 148 * 6 * 256
+    g = torch.Generator("cuda").manual_seed(T + D)
+    x = torch.randn((T, H, D), generator=g, device="cuda").bfloat16()
+    pos = torch.randint(-5, 2 ** 20, (T,), generator=g, device="cuda")
+    tab = _table(lib, c)
+    got = lib.dsa_rope(x, pos, tab, offset=offset)
+    for t in range(0, T, 97):
+        assert torch.equal(got[t:t + 97], lib.dsa_rope(x[t:t + 97], pos[t:t + 97], tab, offset=offset))
+    some = [0, 1, 2, T // 2, T - 3, T - 2, T - 1]
+    _check(lib, got[some], x[some], pos[some].cpu(), c, tab)
+    kept = x.clone()
+    lib.dsa_rope(x, pos, tab, offset=offset, out=x)
+    assert torch.equal(x, got)
+    rest = torch.ones(D, dtype=torch.bool, device="cuda")
+    rest[offset:offset + rot] = False
+    assert torch.equal(got[..., rest], kept[..., rest])
