@@ -8,7 +8,7 @@ owns segments r and 2R-1-r.  A token's indexer and attention work grow with its
 position, so pairing an early segment with a late one gives every rank the
 same causal work.
 
-Each rank holds the index keys (FP8 codes + scales, or bf16) and latent rows
+Each rank holds the index keys (FP8 or FP4 codes + scales, or bf16) and latent rows
 (bf16, or FP8 codes + tile-scale bytes) of its own two segments, segment r
 first.  One all-gather per pool (NCCL over NVLink, into each rank's own
 memory) gives every rank the pools of the whole sequence laid out rank by
@@ -107,9 +107,9 @@ def cp_prefill(plan: ZigzagPlan, group, qI, w, q, kI_local, kI_scale_local, kv_l
 
     qI [2 seg, 64, 128], w [2 seg, 64], q [2 seg, H, 576]: this rank's query
     tokens in local order; kI_local [2 seg, 128] (+ kI_scale_local [2 seg],
-    [2 seg, 4] for MXFP8, or None) and kv_local [2 seg, 576] (+ kv_scale_local
-    [2 seg, 8] for the FP8 latent cache, or None): its rows of the pools, same
-    order.  `attend(seqs, qI, w, kI, kI_scale, q, kv, K, scale[, kv_scale=])`
+    [2 seg, 4] for MXFP8, or None; MXFP4: [2 seg, 64] and [2 seg, 4]) and kv_local
+    [2 seg, 576] (+ kv_scale_local [2 seg, 8] for the FP8 latent cache, or None): its
+    rows of the pools, same order.  `attend(seqs, qI, w, kI, kI_scale, q, kv, K, scale[, kv_scale=])`
     -> (out, lse) runs the hot path (default: dsa_index_topk_attn; kv_scale is
     passed only for the FP8 latent cache).  Returns (out, lse) of the whole
     sequence in order when gather_output, else this rank's rows (local order).
