@@ -40,7 +40,7 @@
 // additions commute, so the result does not depend on the order of the atomics.
 //
 // What bounds it (warm, one B200): 400 tokens of 2048 rows take 139 us with 128 heads
-// (834 TFLOP/s, 51 % of the measured bf16 rate: MMAs of a tile against its issue, and
+// (869 TFLOP/s, 53 % of the measured bf16 rate: MMAs of a tile against its issue, and
 // three waves of CTAs for 2.7) and 96 us with 64 (the gather: 10 TB/s out of L2); over
 // the FP8 cache 64 heads take 115 us (the sums: two terms per head).  A decode step of 8
 // tokens takes 9 us: one block per CTA, the chain of its steps.

@@ -33,9 +33,11 @@
 //    the second halves, each the A operand of a tile (half the steps per key).
 //    8 x 131,072 keys take 24.7 us: 71 MB (11 us at the measured copy rate), 4.5 us
 //    until the plan is there and the first stage has landed, and pages that arrive at
-//    3.5 TB/s (22 us without the epilogue's products).  1000-token prompts at 8 K take
-//    174 us, bound by the epilogue's 64 maxima per score (ALU pipe 59 % busy; 113 us
-//    without maxima and products).
+//    3.5 TB/s (22 us without the epilogue's products; why the pages come no faster
+//    is open).  1000-token prompts at 8 K take 171 us, where the products alone
+//    would take 36 at four times the measured bf16 rate: the epilogue bounds them.  No
+//    pipe of it is full (ALU 59 % busy); without maxima and products 113 us remain,
+//    loads from TMEM with their waits and the hand-over of the accumulators.
 //  * warp 2: allocates and frees TMEM (MXFP4: also issues each stage's second tile).
 //  * warps 4-11: epilogue, two warpgroups sharing the tiles.  Thread r
 //    of a warpgroup owns TMEM lane r = key row r, so the ReLU, the head
@@ -111,7 +113,7 @@ struct IdxCfg {
   // barrier arithmetic, TMA and scale copies) outlast the tile's transfer.  An even
   // ring gives each stage to one of them, which waits for its uses in order (a
   // barrier's parity tells the next phase from this one only).  MXFP4, 8 x 131,072
-  // keys: 36.4 us with one, 29.6 with two.
+  // keys: 36.4 us with one, 29.6 with two; E4M3, 8192 tokens: 654 and 651.
   static constexpr int NPROD = NS % 2 == 0 && !kFused ? 2 : 1;
   // Two epilogue warpgroups (from warp 4).  With MXFP4's two tokens per group each
   // takes one token of every tile, else each every other tile: an MXFP4 thread then
@@ -125,7 +127,7 @@ struct IdxCfg {
   static constexpr int TILE_WGS = kMx4 && TG == 2 ? 1 : 2;  // tile i -> the warpgroups that are i mod TILE_WGS
   static constexpr int TOKEN_WGS = NWG / TILE_WGS;         // which then take the group's tokens in turn
   static constexpr bool PIPED = kMx4;                      // see the epilogue
-  // How the CTAs share the work items: a prompt's groups end in items of one to eight
+  // How the CTAs share the work items: a prompt's groups end in items of one to sixteen
   // tiles, and contiguous runs of equally many items left the slowest SM with 16 %
   // more than the mean (1000-token prompts 187 -> 174 us).
   static constexpr bool SPREAD = kMx4 && TG > 1;
