@@ -42,6 +42,12 @@ L2_FLUSH_BYTES = 256 << 20
 # figure back into null.
 NCU_CAPTURES = (
     # kernel, config keys that must match, bytes per launch, sources, digest
+    ("index_scores", {"index_cache": "fp8_e4m3"}, 146.48e6, ("k_indexer.cu",), "ba8c8bd51600bfb6"),
+    ("index_scores", {"index_cache": "mxfp8"}, 145.90e6, ("k_indexer.cu",), "ba8c8bd51600bfb6"),
+    ("index_scores", {"index_cache": "mxfp4"}, 72.96e6, ("k_indexer.cu",), "ba8c8bd51600bfb6"),
+    ("topk_filter", {}, 4.35e6, ("k_topk.cu",), "bccc25991fbcb383"),
+    ("sparse_mla", {"latent_cache": "bf16"}, 20.28e6, ("k_sparse_mla.cu",), "63241dbf0bd535ee"),
+    # of earlier sources, which they still describe
     ("index_scores", {"index_cache": "fp8_e4m3"}, 145.60e6, ("k_indexer.cu",), "6a6254d29a2242f3"),
     ("index_scores", {"index_cache": "mxfp8"}, 144.81e6, ("k_indexer.cu",), "6a6254d29a2242f3"),
     ("topk_filter", {}, 4.35e6, ("k_topk.cu",), "507b32e02ae94d9e"),
@@ -65,8 +71,8 @@ def ncu_traffic(kernel: str, config: dict):
     line's config object), or None if not captured for it or stale."""
     for name, keys, nbytes, files, digest in NCU_CAPTURES:
         want = {**NCU_WORKLOAD, **keys}
-        if name == kernel and all(config.get(k) == v for k, v in want.items()):
-            return nbytes if source_digest(files) == digest else None
+        if name == kernel and all(config.get(k) == v for k, v in want.items()) and source_digest(files) == digest:
+            return nbytes
     return None
 
 
