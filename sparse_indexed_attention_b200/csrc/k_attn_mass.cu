@@ -39,11 +39,12 @@
 // token's whole attention, 8.4 million tokens before it overflows): integer
 // additions commute, so the result does not depend on the order of the atomics.
 //
-// What bounds it (warm, one B200): 400 tokens of 2048 rows take 139 us with 128 heads
+// What bounds it (warm, one B200): 400 tokens of 2048 of 2300 rows take 139 us with 128 heads
 // (869 TFLOP/s, 53 % of the measured bf16 rate: MMAs of a tile against its issue, and
 // three waves of CTAs for 2.7) and 96 us with 64 (the gather: 10 TB/s out of L2); over
-// the FP8 cache 64 heads take 115 us (the sums: two terms per head).  A decode step of 8
-// tokens takes 9 us: one block per CTA, the chain of its steps.
+// the FP8 cache 64 heads take 115 us and 128 heads 199 (the sums: two terms per head).  A
+// decode step of 8 tokens takes 8 to 9 us (FP8 cache: 10 with 64 heads, 16 with 128): one
+// block per CTA, the chain of its steps.
 #include "kv8.cuh"
 #include "sm100.cuh"
 #include "tensor_map.cuh"
