@@ -8,13 +8,12 @@ raises.
 
 Functions carry the C names (``dsa_index_scores`` ...).  Outputs not passed in
 are allocated with torch on the inputs' device; workspaces are allocated
-zeroed and cached per device, op, host thread and stream, unless one is passed in.
+zeroed and cached per (device, stream, op), unless one is passed in.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import threading
 from dataclasses import dataclass
 
 import torch
@@ -282,53 +281,56 @@ def dsa_workspace_size(op: int, seqs: Seqs | None = None, K: int = 1, H: int = 1
     return int(_lib.dsa_workspace_size(op, ctypes.byref(c), K, H))
 
 
-_ws_own = threading.local()     # .cache: (device, stream, key) -> buffer
-_ws_newest: dict = {}           # (device, key) -> the buffer made last, by whatever thread and for whatever stream
+_ws_cache: dict = {}            # (device, stream, key) -> buffer
+_ws_newest: dict = {}           # (device, key) -> the buffer made last, for whatever stream
 _ws_captured: dict = {}
 
 
 def workspace(nbytes: int, device, key=None) -> torch.Tensor:
     """A zeroed device workspace of at least nbytes, cached per (device, key) for
-    the calling thread and the device's current stream.
+    the device's current stream.
 
     The calls' keys: "index_scores", "topk", "sparse_mla", "index_topk_attn",
     "append_index_keys", "attn_mass", "evict_select" and "evict_compact".
     workspace(0, device, key) is the buffer whose error flag dsa_check_error
-    reads: that of this thread and stream, or the newest if they have none.
+    reads: that of the current stream, or the newest if it has none.
 
-    Every call that is not given `ws` uses this buffer, so that calls of two
-    threads or streams do not share one (the library requires that of concurrent
-    calls: scratch and sticky error flag are in it).
+    Every call that is not given `ws` uses this buffer, so that calls on two
+    streams do not share one (the library requires that of concurrent calls:
+    scratch and sticky error flag are in it).  Calls of several host threads on
+    one stream share one in turn: the binding launches each call as a whole.
 
-    During stream capture the newest buffer serves where the capturing stream has none,
-    and one that has to be made belongs to the graph alone (its zeroing is part
-    of the graph and has not run), so it is not cached.  A graph that is replayed
-    beside other calls or graphs, or whose error flag is to be read, is captured
-    with a workspace of its own.  A cached buffer that a capture uses stays alive
-    when a larger one replaces it: the graph still writes to it."""
+    During stream capture another stream's buffer serves where the capturing one has
+    none that is large enough, and one that has to be made belongs to the graph
+    alone (its zeroing is part of the graph and has not run), so it is not
+    cached.  A graph that is replayed beside other calls or graphs, or whose error
+    flag is to be read, is captured with a workspace of its own.  A cached buffer
+    that a capture uses stays alive when a larger one replaces it: the graph still
+    writes to it."""
     if not isinstance(device, torch.device):
         device = torch.device(device)
     capturing = False
     if device.type == "cuda":
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        k = (device.index, torch._C._cuda_getCurrentRawStream(device.index), key)
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        stream = _binding.stream_of(device)
+        if stream is None:
+            capturing, stream = True, _stream(device)
+        k = (device.index, stream, key)
     else:
         k = (device, None, key)
-    try:
-        cache = _ws_own.cache
-    except AttributeError:
-        cache = _ws_own.cache = {}
-    ws = cache.get(k)
-    if ws is None and (capturing or nbytes == 0):
+    ws = _ws_cache.get(k)
+    if ws is None and nbytes == 0:
         ws = _ws_newest.get((device, key))
+    if capturing and (ws is None or ws.numel() < nbytes):
+        ws = max((b for (d, _, name), b in list(_ws_cache.items()) if d == device.index and name == key),
+                 key=lambda b: b.numel(), default=None)
     if ws is None or ws.numel() < nbytes:
         small, ws = ws, torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         if not capturing:
             if small is not None:
                 ws[:4].copy_(small[:4])     # an error that was not read yet
-            cache[k] = _ws_newest[device, key] = ws
+            _ws_cache[k] = _ws_newest[device, key] = ws
     elif capturing:
         _ws_captured[ws.data_ptr()] = ws
     return ws

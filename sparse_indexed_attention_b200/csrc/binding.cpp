@@ -16,14 +16,17 @@
 //   rows(t, dtype, device) -> (T, H, D, token stride, head stride) or None
 //   pools(list, pages, device) -> (bytes of dsa_pool_t[], new pages) or None
 //   empty(shape, dtype, device) -> tensor
+//   stream_of(device) -> the current stream's address, or None while it captures
 // and every asynchronous entry point under its C name, called as
 //   dsa_x(device, arguments without the stream) -> status
 // which makes `device` current, appends its current stream and releases the GIL.
+// Host threads that call on one stream do so in turn.
 // A pointer argument is a tensor, None or an address; dsa_seqs_t a Seqs.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Device.h>
@@ -33,6 +36,7 @@
 
 #include <algorithm>
 #include <limits>
+#include <mutex>
 #include <string>
 #include <tuple>
 #include <type_traits>
@@ -250,6 +254,18 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+PyObject* stream_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  at::Device device(at::kCPU);
+  if (!count("stream_of", n, 1) || !device_of(a[0], device)) return nullptr;
+  const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  C10_CUDA_CHECK(cudaStreamIsCapturing(stream, &status));
+  if (status != cudaStreamCaptureStatusNone) Py_RETURN_NONE;
+  return PyLong_FromVoidPtr(stream);
+  END_HANDLE_TH_ERRORS
+}
+
 // One argument of a call, converted from its Python object.
 template <class T, class = void>
 struct Arg;
@@ -362,6 +378,14 @@ PyObject* workspace_size(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A call may be several launches over one workspace, which a stream's calls share:
+// they must not mix with another thread's.  (Streams that fall on one lock wait for
+// each other's launches, no more.)
+std::mutex& launching_on(dsa_stream_t stream) {
+  static std::mutex locks[64];
+  return locks[(reinterpret_cast<uintptr_t>(stream) >> 4) % 64];
+}
+
 // The last parameter of an entry point, the stream, comes from the device.
 template <auto F, class... A, size_t... I>
 PyObject* call(std::tuple<Arg<A>...>& args, PyObject* const* a, Py_ssize_t n, std::index_sequence<I...>) {
@@ -383,7 +407,10 @@ PyObject* call(std::tuple<Arg<A>...>& args, PyObject* const* a, Py_ssize_t n, st
   }
   long status;
   Py_BEGIN_ALLOW_THREADS
-  status = static_cast<long>(F(std::get<I>(args).value..., stream));
+  {
+    std::lock_guard<std::mutex> one(launching_on(stream));
+    status = static_cast<long>(F(std::get<I>(args).value..., stream));
+  }
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(status);
 }
@@ -413,6 +440,7 @@ PyMethodDef methods[] = {
     DSA_METHOD("rows", &rows),
     DSA_METHOD("pools", &pools),
     DSA_METHOD("empty", &empty),
+    DSA_METHOD("stream_of", &stream_of),
     DSA_ENTRY(dsa_quantize_index_query),
     DSA_ENTRY(dsa_quantize_index_query_mx),
     DSA_ENTRY(dsa_quantize_index_query_mx4),

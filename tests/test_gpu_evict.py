@@ -442,6 +442,7 @@ def test_default_workspace_tells_of_a_refused_page(lib):
     """The error flag of calls without a workspace is where the other operators have it,
     whatever the pools' sizes."""
     flag = lambda: lib.dsa_check_error(lib.workspace(0, "cuda", "evict_compact"))  # noqa: E731
+    flag()                                         # what calls before this test have left
     for ctx in ([300, 200], [70], [30000, 5]):
         table, new_table, total = _cache(ctx, 1)
         seqs = _seqs(lib, ctx, table, total)

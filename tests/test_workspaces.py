@@ -1,5 +1,5 @@
-"""The workspaces of calls that are given none: one per thread and stream, so that
-calls at the same time do not write into each other's scratch."""
+"""The workspaces of calls that are given none: one per stream, so that calls at the
+same time do not write into each other's scratch."""
 import threading
 
 import numpy as np
@@ -9,29 +9,10 @@ import torch
 import sparse_indexed_attention_b200 as dsa
 
 
-def _in_thread(fn):
-    got = []
-    t = threading.Thread(target=lambda: got.append(fn()))
-    t.start()
-    t.join()
-    return got[0]
-
-
-def test_threads_have_their_own():
-    key = "threads_have_their_own"
-    mine = dsa.workspace(512, "cpu", key)
-    assert dsa.workspace(300, "cpu", key) is mine and dsa.workspace(0, "cpu", key) is mine
-    other = _in_thread(lambda: dsa.workspace(512, "cpu", key))
-    assert other.data_ptr() != mine.data_ptr() and not other.any()
-    assert dsa.workspace(512, "cpu", key) is mine
-
-
-def test_a_look_finds_the_newest_buffer():
-    key = "found_by_a_look"
-    other = _in_thread(lambda: dsa.workspace(512, "cpu", key))
-    assert dsa.workspace(0, "cpu", key) is other          # nothing of this thread's yet
-    mine = dsa.workspace(512, "cpu", key)
-    assert mine is not other and dsa.workspace(0, "cpu", key) is mine
+def test_one_buffer_per_device_and_key():
+    mine = dsa.workspace(512, "cpu", "one_buffer")
+    assert dsa.workspace(300, "cpu", "one_buffer") is mine and dsa.workspace(0, "cpu", "one_buffer") is mine
+    assert dsa.workspace(512, "cpu", "another") is not mine
 
 
 @pytest.mark.gpu
@@ -41,10 +22,13 @@ def test_streams_have_their_own():
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         assert dsa.workspace(0, "cuda", key) is mine      # a look before the stream has one
-        other = dsa.workspace(512, "cuda", key)
+        other = dsa.workspace(4096, "cuda", key)
         assert other.data_ptr() != mine.data_ptr()
         assert dsa.workspace(512, "cuda", key) is other and dsa.workspace(0, "cuda", key) is other
     assert dsa.workspace(512, "cuda", key) is mine and dsa.workspace(0, "cuda", key) is mine
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):        # the capturing stream has none: a large enough one
+        assert dsa.workspace(2048, "cuda", key) is other
+        torch.zeros(1, device="cuda")
 
 
 class _Batch:
@@ -86,40 +70,43 @@ class _Batch:
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("threads", [False, True])
-def test_two_at_once_without_workspaces(threads):
+@pytest.mark.parametrize("how", ["two streams", "two threads", "two threads on one stream"])
+def test_two_at_once_without_workspaces(how):
     batches = [_Batch(s) for s in (1, 2)]
     want = [b.run(2) for b in batches]
     torch.cuda.synchronize()
-    got, wrong = [None, None], []
+    streams = [torch.cuda.Stream() for _ in batches]
+    if how == "two threads on one stream":
+        streams[1] = streams[0]
+    got, wrong = [[], []], []
 
     def work(i):
         try:
-            with torch.cuda.stream(torch.cuda.Stream()):
+            with torch.cuda.stream(streams[i]):
                 torch.cuda._sleep(2_000_000)              # the streams' work overlaps
-                got[i] = batches[i].run()
-                torch.cuda.current_stream().synchronize()
-                assert dsa.dsa_check_error(dsa.workspace(0, "cuda", "index_scores")) == dsa.DSA_OK
-                assert dsa.dsa_check_error(dsa.workspace(0, "cuda", "evict_compact")) == dsa.DSA_ERR_BAD_INDEX
+                got[i] = batches[i].run(40)
         except BaseException as e:  # noqa: BLE001 (a thread's failure is the test's)
             wrong.append(e)
-    if threads:
+    if how == "two streams":
+        for _ in range(20):
+            for i, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    torch.cuda._sleep(50_000)
+                    got[i] += batches[i].run(2)
+    else:
         ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
         for t in ts:
             t.start()
         for t in ts:
             t.join()
-    else:
-        streams = [torch.cuda.Stream() for _ in batches]
-        got = [[], []]
-        for _ in range(10):
-            for i, s in enumerate(streams):
-                with torch.cuda.stream(s):
-                    torch.cuda._sleep(50_000)
-                    got[i] += batches[i].run(2)
-    torch.cuda.synchronize()
     assert not wrong, wrong
+    for s in streams[:1 if streams[0] is streams[1] else 2]:
+        with torch.cuda.stream(s):
+            assert dsa.dsa_check_error(dsa.workspace(0, "cuda", "index_scores")) == dsa.DSA_OK
+            assert dsa.dsa_check_error(dsa.workspace(0, "cuda", "evict_compact")) == dsa.DSA_ERR_BAD_INDEX
+    torch.cuda.synchronize()
     for a, b in zip(want, got):
+        assert len(b) == 80
         for i, x in enumerate(b):
             assert torch.equal(x, a[i % 4]), i
 
